@@ -328,6 +328,117 @@ TTQ_API ttq_status ttq_prompt_attention(const void* qkv_bf16, int64_t T, int64_t
                                         int64_t head_dim, const void* k_cache_bf16, const void* v_cache_bf16,
                                         int64_t cache_len, void* out_bf16, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------------
+ * Serving several sequences from a paged cache. The prompt's codes are per prompt, so
+ * sequences that share a prompt (branches of one prompt, later turns) share its codes; these
+ * entry points give them a cache made of pages, attention of one or many new tokens per
+ * sequence over it, the upkeep of the pages and the probabilities of the answer.
+ *
+ *   k_pages, v_pages  device bf16 [num_pages, page_size, kv_heads, head_dim] (one layer)
+ *   page_table        device int32 [seqs, table_width]: position p of sequence b lies in row
+ *                     p % page_size of page page_table[b][p / page_size]; entries past the
+ *                     sequence's last page are not read
+ *   q_start           device int32 [seqs + 1]: the new tokens of sequence b are rows
+ *                     q_start[b] .. q_start[b+1]-1 of the token arrays (q_start[0] = 0, never
+ *                     decreasing, at most `tokens`); rows past q_start[seqs] are padding and
+ *                     are neither read nor written
+ *   kv_len            device int32 [seqs]: positions of sequence b, its new tokens included;
+ *                     new token i of n is at position kv_len - n + i
+ * A value read on the device that is out of range (a table entry that is no page, lengths
+ * that contradict the sizes given here) makes no access outside the buffers;
+ * ttq_device_status() then reports TTQ_ERR_INVALID_ARG and the rows concerned are
+ * unspecified. page_size in {16, 32, 64, 128, 256}; num_pages * page_size < 2^31.
+ * --------------------------------------------------------------------------------- */
+
+/* Plan of one step's attention, used by every layer of the step: the split of the work over
+ * the GPU, made on the device from the step's lengths (so a captured CUDA graph replays it on
+ * new lengths).
+ *   tokens    rows of the token arrays;  max_new  the most new tokens of any sequence
+ *   prefix    NULL, or device int32 [seqs]: the first prefix[b] positions are visible to every
+ *             new token of b (also those ahead of it and those outside the window)
+ *   window    0, or the number of positions a token sees at most: its own and the window - 1
+ *             before it
+ *   plan      device buffer of ttq_attention_plan_size() bytes: the plan and the scratch of
+ *             ttq_paged_attention, so one call at a time may use it
+ * Calls of ttq_paged_attention with this plan must be given the same sizes. seqs <= 65536;
+ * tokens <= 2^24; kv_len <= 2^30. heads / kv_heads <= 64 (any integer). head_dim 64 or 128. */
+TTQ_API ttq_status ttq_attention_plan_size(int64_t seqs, int64_t tokens, int64_t max_new, int64_t heads,
+                                           int64_t kv_heads, int64_t head_dim, size_t* bytes);
+TTQ_API ttq_status ttq_attention_plan(const int32_t* q_start, const int32_t* kv_len, const int32_t* prefix,
+                                      int64_t window, int64_t seqs, int64_t tokens, int64_t max_new, int64_t heads,
+                                      int64_t kv_heads, int64_t head_dim, void* plan, size_t plan_bytes,
+                                      cudaStream_t stream);
+
+/* Attention of every sequence's new tokens over its pages (grouped-query; k and v of kv head
+ * h / (heads / kv_heads)); the new tokens' own k and v are in the pages already:
+ *   out[t, h] = sum_k softmax_k(s_k) v_k over the visible positions k of token t, with
+ *   s_k = q_t,h . k_k / sqrt(head_dim),  then  softcap * tanh(s_k / softcap)  when softcap > 0,
+ *   then  s_k + slopes[h] * (k - position of t)  when slopes != NULL.
+ * Visible are the positions up to the token's own (inside the window) and the prefix, as in
+ * the plan. A token that sees no position (kv_len below the number of new tokens) gets zeros.
+ *   q        device bf16, row t at q + t * ld_q elements, its first heads * head_dim
+ *            channels (ld_q % 8 == 0)
+ *   slopes   NULL, or device fp32 [heads]
+ *   out      device bf16 [tokens, heads * head_dim], not overlapping q
+ * k and v at visible positions must be finite; what pages hold past kv_len is never used. */
+TTQ_API ttq_status ttq_paged_attention(const void* q_bf16, int64_t ld_q, int64_t seqs, int64_t tokens,
+                                       int64_t max_new, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                       const void* k_pages_bf16, const void* v_pages_bf16, int64_t num_pages,
+                                       int64_t page_size, const int32_t* page_table, int64_t table_width,
+                                       float softcap, const float* slopes, void* out_bf16, void* plan,
+                                       size_t plan_bytes, cudaStream_t stream);
+
+/* ttq_qk_norm_rope for a paged cache: the same arithmetic, with every token's position and
+ * pages taken from its sequence, and q written to its own buffer (qkv is only read).
+ *   qkv       device bf16 [tokens, (heads + 2 kv_heads) * head_dim]
+ *   q_out     device bf16 [tokens, heads * head_dim], not overlapping qkv
+ *   rope_table device fp32 from ttq_rope_table; a position past its table_positions rows, or
+ *             past the page table, writes nothing and is reported by ttq_device_status()
+ * Pages that two sequences share must not be among those written. head_dim in {64, 128, 256}. */
+TTQ_API ttq_status ttq_qk_norm_rope_paged(const void* qkv_bf16, int64_t seqs, int64_t tokens, int64_t heads,
+                                          int64_t kv_heads, int64_t head_dim, const void* q_norm_bf16,
+                                          const void* k_norm_bf16, float eps, const float* rope_table,
+                                          int64_t table_positions, const int32_t* q_start, const int32_t* kv_len,
+                                          void* k_pages_bf16, void* v_pages_bf16, int64_t num_pages,
+                                          int64_t page_size, const int32_t* page_table, int64_t table_width,
+                                          void* q_out_bf16, cudaStream_t stream);
+
+/* Copies pages src[i] -> dst[i] of both pools in every layer (forking a shared last page,
+ * compaction). Pools: `layers` layers of num_pages pages of page_bytes bytes each, contiguous.
+ * Every destination appears once and is no source of another pair; a pair with src[i] == dst[i]
+ * does nothing, a pair out of range is skipped and reported by ttq_device_status().
+ *   src, dst  device int32 [pairs];  page_bytes % 16 == 0 */
+TTQ_API ttq_status ttq_copy_pages(void* k_pool, void* v_pool, int64_t layers, int64_t num_pages, int64_t page_bytes,
+                                  const int32_t* src, const int32_t* dst, int64_t pairs, cudaStream_t stream);
+
+/* out[i] = mapping[table[i]] for entries that are pages, table[i] for negative ones (the page
+ * tables after a compaction). An entry past num_pages, or mapped past them, becomes -1 and is
+ * reported by ttq_device_status().
+ *   table, out  device int32 [entries] (out may be table);  mapping  device int32 [num_pages] */
+TTQ_API ttq_status ttq_remap_pages(const int32_t* table, int64_t entries, const int32_t* mapping, int64_t num_pages,
+                                   int32_t* out, cudaStream_t stream);
+
+typedef enum { TTQ_BF16 = 0, TTQ_FP16 = 1, TTQ_FP32 = 2 } ttq_dtype;
+
+/* Log probabilities of given tokens from logits, with the entropy of each row's distribution
+ * and its `top` most likely tokens: with p = softmax(x) over a row's `vocab` logits,
+ *   logprob[r] = log p[tokens[r]]   (0 where tokens[r] < 0: a padding row)
+ *   entropy[r] = -sum p log p       (nats)
+ *   top_ids[r], top_logprobs[r]     in falling order, equal logits by rising index
+ *   logits   device, row r at element r * ld (ld >= vocab), of type `dtype`; 16-byte aligned base
+ *   tokens   device int64 [rows]; a token past the vocabulary gives NaN and is reported by
+ *            ttq_device_status()
+ *   top_ids  device int64 [rows, top], top_logprobs device fp32 [rows, top]; NULL when top = 0
+ *   ws       device scratch of ttq_token_logprobs_workspace_size() bytes
+ * A logit of -inf is a token of probability zero. A row with a NaN or +inf logit, or with
+ * nothing but -inf, has NaN probabilities and entropy; its top_ids stay in the order of its
+ * logits, NaN after everything else. 0 <= top <= min(32, vocab); vocab <= 2^20; rows < 2^31. */
+TTQ_API ttq_status ttq_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int64_t top, size_t* bytes);
+TTQ_API ttq_status ttq_token_logprobs(const void* logits, ttq_dtype dtype, int64_t rows, int64_t vocab, int64_t ld,
+                                      const int64_t* tokens, int64_t top, float* logprob, float* entropy,
+                                      int64_t* top_ids, float* top_logprobs, void* ws, size_t ws_bytes,
+                                      cudaStream_t stream);
+
 /* *pos_dev += n on the device, in stream order (moves a captured decode step to the next
  * position). */
 TTQ_API ttq_status ttq_position_advance(int64_t* pos_dev, int64_t n, cudaStream_t stream);

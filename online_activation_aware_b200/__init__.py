@@ -11,9 +11,12 @@ Functions keep the C names without the ``ttq_`` prefix:
 ``linear_decode``, ``linear_decode_batched``, ``workspace_size``,
 ``codes_words``, ``device_status``, ``set_wait_limit_ns``, and the decoder-layer kernels
 ``rmsnorm``, ``rope_table``, ``qk_norm_rope``, ``silu_mul``, ``prompt_attention``,
-``decode_attention``, ``position_advance``. ``TTQLinear`` bundles one
+``decode_attention``, ``position_advance``; for several sequences over a paged cache
+``AttentionPlan``, ``paged_attention``, ``qk_norm_rope_paged``, ``copy_pages``, ``remap_pages``,
+and ``token_logprobs`` for the answer. ``TTQLinear`` bundles one
 layer's weight and the per-prompt buffers (prefill, then decode reusing the codes);
-``online_activation_aware_b200.decoder`` chains them into a decoder stack.
+``online_activation_aware_b200.decoder`` chains them into a decoder stack, and
+``online_activation_aware_b200.paged`` into one whose sequences share a prompt.
 """
 
 from __future__ import annotations
@@ -93,6 +96,24 @@ def load_library(path: str = LIB_PATH):
     lib.ttq_decode_attention.restype = i32
     lib.ttq_prompt_attention.argtypes = [vp, i64, i64, i64, i64, vp, vp, i64, vp, vp]
     lib.ttq_prompt_attention.restype = i32
+    lib.ttq_attention_plan_size.argtypes = [i64, i64, i64, i64, i64, i64, ctypes.POINTER(sz)]
+    lib.ttq_attention_plan_size.restype = i32
+    lib.ttq_attention_plan.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, vp, sz, vp]
+    lib.ttq_attention_plan.restype = i32
+    lib.ttq_paged_attention.argtypes = [vp, i64, i64, i64, i64, i64, i64, i64, vp, vp, i64, i64, vp, i64, f32, vp, vp,
+                                        vp, sz, vp]
+    lib.ttq_paged_attention.restype = i32
+    lib.ttq_qk_norm_rope_paged.argtypes = [vp, i64, i64, i64, i64, i64, vp, vp, f32, vp, i64, vp, vp, vp, vp, i64, i64,
+                                           vp, i64, vp, vp]
+    lib.ttq_qk_norm_rope_paged.restype = i32
+    lib.ttq_copy_pages.argtypes = [vp, vp, i64, i64, i64, vp, vp, i64, vp]
+    lib.ttq_copy_pages.restype = i32
+    lib.ttq_remap_pages.argtypes = [vp, i64, vp, i64, vp, vp]
+    lib.ttq_remap_pages.restype = i32
+    lib.ttq_token_logprobs_workspace_size.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
+    lib.ttq_token_logprobs_workspace_size.restype = i32
+    lib.ttq_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, sz, vp]
+    lib.ttq_token_logprobs.restype = i32
     lib.ttq_position_advance.argtypes = [vp, i64, vp]
     lib.ttq_position_advance.restype = i32
     lib.ttq_silu_mul.argtypes = [vp, i64, i64, vp, vp]
@@ -515,4 +536,214 @@ def silu_mul(gate_up, out=None, stream=None):
         out = torch.empty(rows, inter, dtype=torch.bfloat16, device=gate_up.device)
     _check("ttq_silu_mul", load_library().ttq_silu_mul(
         _ptr(gate_up, torch.bfloat16, "gate_up"), rows, inter, _ptr(out, torch.bfloat16, "out"), _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------ paged cache, several sequences
+
+
+def _device_of(**tensors):
+    """The CUDA device all the given tensors (None skipped) are on."""
+    import torch
+
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+    return torch.cuda.device(dev)
+
+
+def _shape(t, name, *dims):
+    """Raises unless t has the given sizes (None: any)."""
+    if t is not None and (t.dim() != len(dims) or any(d is not None and d != n for d, n in zip(dims, t.shape))):
+        raise ValueError(f"{name} must have shape {list(dims)}, got {list(t.shape)}")
+
+
+def _pool(k_pages, v_pages, page_table, seqs: int, kv_heads: int, head_dim: int):
+    _shape(k_pages, "k_pages", None, None, kv_heads, head_dim)
+    _shape(v_pages, "v_pages", *k_pages.shape)
+    _shape(page_table, "page_table", seqs, None)
+
+
+class AttentionPlan:
+    """Plan of one step's attention over a paged cache, shared by every layer of the step.
+
+    Made for ``seqs`` sequences with ``tokens`` rows of new tokens in all, at most ``max_new``
+    (default: ``tokens``) of them in one sequence. ``update`` plans a step from its lengths on
+    the device, on the stream it is called on (in a captured graph it plans anew at every
+    replay). The plan's buffer is also the scratch of ``paged_attention``: one call at a time
+    uses it."""
+
+    def __init__(self, seqs: int, tokens: int, heads: int, kv_heads: int, head_dim: int, max_new: int | None = None,
+                 device="cuda"):
+        import torch
+
+        self.seqs, self.tokens = int(seqs), int(tokens)
+        self.max_new = self.tokens if max_new is None else int(max_new)
+        self.heads, self.kv_heads, self.head_dim = int(heads), int(kv_heads), int(head_dim)
+        n = ctypes.c_size_t(0)
+        _check("ttq_attention_plan_size", load_library().ttq_attention_plan_size(
+            self.seqs, self.tokens, self.max_new, self.heads, self.kv_heads, self.head_dim, ctypes.byref(n)))
+        self.buffer = torch.zeros(int(n.value), dtype=torch.uint8, device=device)
+
+    def update(self, q_start, kv_len, window: int = 0, prefix=None, stream=None):
+        """Plans a step: sequence b's new tokens are rows q_start[b] .. q_start[b+1] - 1, its
+        cache holds kv_len[b] positions with them (int32 tensors). ``window`` > 0 limits every
+        token to that many positions; the first prefix[b] positions stay visible to all."""
+        import torch
+
+        _shape(q_start, "q_start", self.seqs + 1)
+        _shape(kv_len, "kv_len", self.seqs)
+        _shape(prefix, "prefix", self.seqs)
+        with _device_of(q_start=q_start, kv_len=kv_len, prefix=prefix, plan=self.buffer):
+            _check("ttq_attention_plan", load_library().ttq_attention_plan(
+                _ptr(q_start, torch.int32, "q_start"), _ptr(kv_len, torch.int32, "kv_len"),
+                _ptr(prefix, torch.int32, "prefix"), window, self.seqs, self.tokens, self.max_new, self.heads,
+                self.kv_heads, self.head_dim, _ptr(self.buffer), self.buffer.numel(), _stream(stream)))
+        return self
+
+
+def paged_attention(q, plan: AttentionPlan, k_pages, v_pages, page_table, softcap: float = 0.0, slopes=None, out=None,
+                    stream=None):
+    """Attention of every sequence's new tokens over its pages. q [tokens, >= heads * head_dim]
+    bf16 (rows may be strided: the stacked projection works), k_pages / v_pages
+    [num_pages, page_size, kv_heads, head_dim] bf16, page_table [seqs, width] int32. Scores are
+    capped to softcap * tanh(s / softcap) when softcap > 0, then biased by slopes[h] * (k - pos).
+    Returns out [tokens, heads * head_dim] bf16; rows past the last sequence are not written."""
+    import torch
+
+    H, D = plan.heads, plan.head_dim
+    _pool(k_pages, v_pages, page_table, plan.seqs, plan.kv_heads, D)
+    _shape(slopes, "slopes", H)
+    _shape(q, "q", plan.tokens, None)
+    if q.shape[1] < H * D or q.stride(1) != 1:
+        raise ValueError(f"q must have at least {H * D} contiguous channels a row")
+    _shape(out, "out", plan.tokens, H * D)
+    with _device_of(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, slopes=slopes, out=out,
+                    plan=plan.buffer):
+        if q.dtype != torch.bfloat16:
+            raise TypeError(f"q must be {torch.bfloat16}, got {q.dtype}")
+        if out is None:
+            out = torch.empty(plan.tokens, H * D, dtype=torch.bfloat16, device=q.device)
+        ld = q.stride(0) if plan.tokens > 1 else max(q.stride(0), H * D)
+        _check("ttq_paged_attention", load_library().ttq_paged_attention(
+            ctypes.c_void_p(q.data_ptr()), ld, plan.seqs, plan.tokens, plan.max_new, H, plan.kv_heads, D,
+            _ptr(k_pages, torch.bfloat16, "k_pages"), _ptr(v_pages, torch.bfloat16, "v_pages"), k_pages.shape[0],
+            k_pages.shape[1], _ptr(page_table, torch.int32, "page_table"), page_table.shape[1], softcap,
+            _ptr(slopes, torch.float32, "slopes"), _ptr(out, torch.bfloat16, "out"), _ptr(plan.buffer),
+            plan.buffer.numel(), _stream(stream)))
+    return out
+
+
+def qk_norm_rope_paged(qkv, heads: int, kv_heads: int, head_dim: int, q_norm, k_norm, eps: float, table, q_start,
+                       kv_len, k_pages, v_pages, page_table, q=None, stream=None):
+    """``qk_norm_rope`` for a paged cache: the new tokens' k (normalised, rotated) and v are
+    written to their sequences' pages at positions kv_len[b] - n .. kv_len[b] - 1, and the
+    normalised, rotated q heads to q [tokens, heads * head_dim], which is returned (qkv is only
+    read; rows past the last sequence are not written)."""
+    import torch
+
+    T = qkv.shape[0]
+    seqs = kv_len.shape[0]
+    _shape(qkv, "qkv", None, (heads + 2 * kv_heads) * head_dim)
+    _pool(k_pages, v_pages, page_table, seqs, kv_heads, head_dim)
+    _shape(q_start, "q_start", seqs + 1)
+    _shape(q_norm, "q_norm", head_dim)
+    _shape(k_norm, "k_norm", head_dim)
+    _shape(table, "table", None, head_dim // 2, 2)
+    _shape(q, "q", T, heads * head_dim)
+    with _device_of(qkv=qkv, q_norm=q_norm, k_norm=k_norm, table=table, q_start=q_start, kv_len=kv_len, k_pages=k_pages,
+                    v_pages=v_pages, page_table=page_table, q=q):
+        if q is None:
+            q = torch.empty(T, heads * head_dim, dtype=torch.bfloat16, device=qkv.device)
+        _check("ttq_qk_norm_rope_paged", load_library().ttq_qk_norm_rope_paged(
+            _ptr(qkv, torch.bfloat16, "qkv"), seqs, T, heads, kv_heads, head_dim, _ptr(q_norm, torch.bfloat16, "q_norm"),
+            _ptr(k_norm, torch.bfloat16, "k_norm"), eps, _ptr(table, torch.float32, "table"), table.shape[0],
+            _ptr(q_start, torch.int32, "q_start"), _ptr(kv_len, torch.int32, "kv_len"),
+            _ptr(k_pages, torch.bfloat16, "k_pages"), _ptr(v_pages, torch.bfloat16, "v_pages"), k_pages.shape[0],
+            k_pages.shape[1], _ptr(page_table, torch.int32, "page_table"), page_table.shape[1],
+            _ptr(q, torch.bfloat16, "q"), _stream(stream)))
+    return q
+
+
+def copy_pages(k_pool, v_pool, src, dst, stream=None):
+    """Copies pages src[i] -> dst[i] of both pools in place, in every layer. Pools
+    [num_pages, page_size, kv_heads, head_dim] or [layers, num_pages, ...], of one type; src and
+    dst int32 tensors on the pools' device. Every destination appears once and is no source of
+    another pair."""
+    import torch
+
+    if k_pool.dim() not in (4, 5):
+        raise ValueError("pools are [num_pages, page_size, kv_heads, head_dim], with the layers ahead or without")
+    _shape(v_pool, "v_pool", *k_pool.shape)
+    layers = k_pool.shape[0] if k_pool.dim() == 5 else 1
+    pages = k_pool.shape[-4]
+    page_bytes = k_pool[..., 0, :, :, :].numel() // layers * k_pool.element_size()
+    _shape(src, "src", None)
+    _shape(dst, "dst", *src.shape)
+    if src.numel() == 0:
+        return
+    with _device_of(k_pool=k_pool, v_pool=v_pool, src=src, dst=dst):
+        _check("ttq_copy_pages", load_library().ttq_copy_pages(
+            _ptr(k_pool, None, "k_pool"), _ptr(v_pool, k_pool.dtype, "v_pool"), layers, pages, page_bytes,
+            _ptr(src, torch.int32, "src"), _ptr(dst, torch.int32, "dst"), src.numel(), _stream(stream)))
+
+
+def remap_pages(table, mapping, out=None, stream=None):
+    """Page tables after their pages moved: out = mapping[table] for entries that are pages,
+    negative entries as they are (int32 tensors; ``out`` may be ``table``)."""
+    import torch
+
+    _shape(mapping, "mapping", None)
+    with _device_of(table=table, mapping=mapping, out=out):
+        if out is None:
+            out = torch.empty_like(table)
+        _shape(out, "out", *table.shape)
+        _check("ttq_remap_pages", load_library().ttq_remap_pages(
+            _ptr(table, torch.int32, "table"), table.numel(), _ptr(mapping, torch.int32, "mapping"), mapping.numel(),
+            _ptr(out, torch.int32, "out"), _stream(stream)))
+    return out
+
+
+def token_logprobs(logits, tokens, top: int = 0, ws=None, stream=None):
+    """Log probabilities of given tokens under softmax(logits) per row, with each row's entropy.
+    logits [rows, vocab] bf16, fp16 or fp32 (rows may be strided), tokens int64 [rows] (negative:
+    a padding row, log probability 0). Returns dict(logprob [rows], entropy [rows]) and, with
+    top > 0, top_ids (int64) and top_logprobs [rows, top]: the most likely tokens in falling
+    order, equal logits by rising index."""
+    import torch
+
+    _shape(logits, "logits", None, None)
+    rows, vocab = logits.shape
+    _shape(tokens, "tokens", rows)
+    if logits.stride(1) != 1 and vocab > 1:
+        raise ValueError("a row's logits must be contiguous")
+    kinds = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    if logits.dtype not in kinds:
+        raise TypeError(f"logits must be bf16, fp16 or fp32, got {logits.dtype}")
+    with _device_of(logits=logits, tokens=tokens, ws=ws):
+        dev = logits.device
+        n = ctypes.c_size_t(0)
+        _check("ttq_token_logprobs_workspace_size", load_library().ttq_token_logprobs_workspace_size(
+            rows, vocab, top, ctypes.byref(n)))
+        if ws is None and n.value > 0:
+            ws = torch.empty(int(n.value), dtype=torch.uint8, device=dev)
+        out = {"logprob": torch.empty(rows, dtype=torch.float32, device=dev),
+               "entropy": torch.empty(rows, dtype=torch.float32, device=dev)}
+        if top > 0:
+            out["top_ids"] = torch.empty(rows, top, dtype=torch.int64, device=dev)
+            out["top_logprobs"] = torch.empty(rows, top, dtype=torch.float32, device=dev)
+        _check("ttq_token_logprobs", load_library().ttq_token_logprobs(
+            ctypes.c_void_p(logits.data_ptr()), kinds[logits.dtype], rows, vocab,
+            logits.stride(0) if rows > 1 else max(logits.stride(0), vocab), _ptr(tokens, torch.int64, "tokens"), top,
+            _ptr(out["logprob"]), _ptr(out["entropy"]), _ptr(out.get("top_ids")), _ptr(out.get("top_logprobs")),
+            _ptr(ws, None, "ws"), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
     return out

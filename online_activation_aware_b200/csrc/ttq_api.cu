@@ -708,6 +708,178 @@ ttq_status ttq_prompt_attention(const void* qkv_bf16, int64_t T, int64_t heads, 
                                                   dev_err(di), stream));
 }
 
+namespace {
+ttq_status check_paged(const ttq::PagedShape& s) {
+  if (s.head_dim != 64 && s.head_dim != 128) return TTQ_ERR_UNSUPPORTED;
+  if (s.heads < 1 || s.kv_heads < 1 || s.heads > 1024 || s.heads % s.kv_heads != 0) return TTQ_ERR_INVALID_ARG;
+  if (s.heads / s.kv_heads > 64) return TTQ_ERR_UNSUPPORTED;
+  if (s.seqs < 1 || s.seqs > 65536 || s.tokens < 1 || s.tokens > (int64_t(1) << 24) || s.max_new < 1 ||
+      s.max_new > s.tokens)
+    return TTQ_ERR_INVALID_ARG;
+  return TTQ_OK;
+}
+// The pools, their page size and the tables.
+ttq_status check_pool(const ttq::PagePool& p, int64_t seqs) {
+  if (!p.k || !p.v || !p.table || p.k == p.v) return TTQ_ERR_INVALID_ARG;
+  if (p.page_size != 16 && p.page_size != 32 && p.page_size != 64 && p.page_size != 128 && p.page_size != 256)
+    return TTQ_ERR_UNSUPPORTED;
+  if (p.num_pages < 1 || p.num_pages >= (int64_t(1) << 31) / p.page_size || p.width < 1 ||
+      p.width > (int64_t(1) << 30) / seqs)
+    return TTQ_ERR_INVALID_ARG;
+  if (!aligned16(p.k) || !aligned16(p.v) || !aligned16(p.table)) return TTQ_ERR_MISALIGNED;
+  return TTQ_OK;
+}
+inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+}  // namespace
+
+ttq_status ttq_attention_plan_size(int64_t seqs, int64_t tokens, int64_t max_new, int64_t heads, int64_t kv_heads,
+                                   int64_t head_dim, size_t* bytes) {
+  if (!bytes) return TTQ_ERR_INVALID_ARG;
+  const ttq::PagedShape s{seqs, tokens, max_new, heads, kv_heads, head_dim};
+  const ttq_status st = check_paged(s);
+  if (st != TTQ_OK) return st;
+  *bytes = round256(ttq::attention_plan_bytes(seqs));
+  return TTQ_OK;
+}
+
+ttq_status ttq_attention_plan(const int32_t* q_start, const int32_t* kv_len, const int32_t* prefix, int64_t window,
+                              int64_t seqs, int64_t tokens, int64_t max_new, int64_t heads, int64_t kv_heads,
+                              int64_t head_dim, void* plan, size_t plan_bytes, cudaStream_t stream) {
+  if (!q_start || !kv_len) return TTQ_ERR_INVALID_ARG;
+  const ttq::PagedShape s{seqs, tokens, max_new, heads, kv_heads, head_dim};
+  ttq_status st = check_paged(s);
+  if (st != TTQ_OK) return st;
+  if (window < 0 || window > (int64_t(1) << 30)) return TTQ_ERR_INVALID_ARG;
+  if (!plan || plan_bytes < ttq::attention_plan_bytes(seqs)) return TTQ_ERR_WORKSPACE;
+  if (!aligned16(q_start) || !aligned16(kv_len) || (prefix && !aligned16(prefix)) || !aligned16(plan))
+    return TTQ_ERR_MISALIGNED;
+  DeviceInfo* di = nullptr;
+  st = device_info(&di);
+  if (st != TTQ_OK) return st;
+  return cuda_status(ttq::launch_attention_plan(q_start, kv_len, prefix, window, s, plan, di->err_word, stream));
+}
+
+ttq_status ttq_paged_attention(const void* q_bf16, int64_t ld_q, int64_t seqs, int64_t tokens, int64_t max_new,
+                               int64_t heads, int64_t kv_heads, int64_t head_dim, const void* k_pages_bf16,
+                               const void* v_pages_bf16, int64_t num_pages, int64_t page_size,
+                               const int32_t* page_table, int64_t table_width, float softcap, const float* slopes,
+                               void* out_bf16, void* plan, size_t plan_bytes, cudaStream_t stream) {
+  if (!q_bf16 || !out_bf16 || q_bf16 == out_bf16) return TTQ_ERR_INVALID_ARG;
+  const ttq::PagedShape s{seqs, tokens, max_new, heads, kv_heads, head_dim};
+  ttq_status st = check_paged(s);
+  if (st != TTQ_OK) return st;
+  const ttq::PagePool p{const_cast<void*>(k_pages_bf16), const_cast<void*>(v_pages_bf16), num_pages, page_size,
+                        page_table, table_width};
+  st = check_pool(p, seqs);
+  if (st != TTQ_OK) return st;
+  if (ld_q < heads * head_dim || ld_q > (int64_t(1) << 30)) return TTQ_ERR_INVALID_ARG;
+  if (!std::isfinite(softcap) || softcap < 0.f) return TTQ_ERR_INVALID_ARG;
+  if (!plan || plan_bytes < ttq::attention_plan_bytes(seqs)) return TTQ_ERR_WORKSPACE;
+  if (!aligned16(q_bf16) || ld_q % 8 != 0 || !aligned16(out_bf16) || !aligned16(plan) ||
+      (slopes && !aligned16(slopes)))
+    return TTQ_ERR_MISALIGNED;
+  DeviceInfo* di = nullptr;
+  st = device_info(&di);
+  if (st != TTQ_OK) return st;
+  return cuda_status(ttq::launch_paged_attention(q_bf16, ld_q, s, p, softcap, slopes, out_bf16, plan, di->err_word,
+                                                 stream));
+}
+
+ttq_status ttq_qk_norm_rope_paged(const void* qkv_bf16, int64_t seqs, int64_t tokens, int64_t heads, int64_t kv_heads,
+                                  int64_t head_dim, const void* q_norm_bf16, const void* k_norm_bf16, float eps,
+                                  const float* rope_table, int64_t table_positions, const int32_t* q_start,
+                                  const int32_t* kv_len, void* k_pages_bf16, void* v_pages_bf16, int64_t num_pages,
+                                  int64_t page_size, const int32_t* page_table, int64_t table_width, void* q_out_bf16,
+                                  cudaStream_t stream) {
+  if (!qkv_bf16 || !q_norm_bf16 || !k_norm_bf16 || !rope_table || !q_start || !kv_len || !q_out_bf16 ||
+      q_out_bf16 == qkv_bf16)
+    return TTQ_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return TTQ_ERR_UNSUPPORTED;
+  if (seqs < 1 || seqs > 65536 || tokens < 1 || tokens > (int64_t(1) << 24) || heads < 1 || kv_heads < 1 ||
+      heads > 1024 || kv_heads > 1024 || table_positions < 1)
+    return TTQ_ERR_INVALID_ARG;
+  const ttq::PagePool p{k_pages_bf16, v_pages_bf16, num_pages, page_size, page_table, table_width};
+  ttq_status st = check_pool(p, seqs);
+  if (st != TTQ_OK) return st;
+  if (!std::isfinite(eps) || !(eps > 0.f)) return TTQ_ERR_INVALID_ARG;
+  if (!aligned16(qkv_bf16) || !aligned16(q_norm_bf16) || !aligned16(k_norm_bf16) || !aligned16(rope_table) ||
+      !aligned16(q_start) || !aligned16(kv_len) || !aligned16(q_out_bf16))
+    return TTQ_ERR_MISALIGNED;
+  DeviceInfo* di = nullptr;
+  st = device_info(&di);
+  if (st != TTQ_OK) return st;
+  const ttq::PagedShape s{seqs, tokens, tokens, heads, kv_heads, head_dim};
+  return cuda_status(ttq::launch_qk_norm_rope_paged(qkv_bf16, s, q_norm_bf16, k_norm_bf16, eps, rope_table,
+                                                    table_positions, q_start, kv_len, p, q_out_bf16, di->err_word,
+                                                    stream));
+}
+
+ttq_status ttq_copy_pages(void* k_pool, void* v_pool, int64_t layers, int64_t num_pages, int64_t page_bytes,
+                          const int32_t* src, const int32_t* dst, int64_t pairs, cudaStream_t stream) {
+  if (!k_pool || !v_pool || !src || !dst || k_pool == v_pool) return TTQ_ERR_INVALID_ARG;
+  if (layers < 1 || layers > 65535 || num_pages < 1 || num_pages > (int64_t(1) << 30) || page_bytes < 16 ||
+      page_bytes > (int64_t(1) << 30) || pairs < 1 || pairs > num_pages)
+    return TTQ_ERR_INVALID_ARG;
+  if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(src) || !aligned16(dst) || page_bytes % 16 != 0)
+    return TTQ_ERR_MISALIGNED;
+  DeviceInfo* di = nullptr;
+  const ttq_status st = device_info(&di);
+  if (st != TTQ_OK) return st;
+  return cuda_status(ttq::launch_copy_pages(k_pool, v_pool, layers, num_pages, page_bytes, src, dst, pairs,
+                                            di->err_word, stream));
+}
+
+ttq_status ttq_remap_pages(const int32_t* table, int64_t entries, const int32_t* mapping, int64_t num_pages,
+                           int32_t* out, cudaStream_t stream) {
+  if (!table || !mapping || !out || out == mapping) return TTQ_ERR_INVALID_ARG;
+  if (entries < 1 || entries > (int64_t(1) << 31) - 256 || num_pages < 1 || num_pages > (int64_t(1) << 30))
+    return TTQ_ERR_INVALID_ARG;
+  if (!aligned16(table) || !aligned16(mapping) || !aligned16(out)) return TTQ_ERR_MISALIGNED;
+  DeviceInfo* di = nullptr;
+  const ttq_status st = device_info(&di);
+  if (st != TTQ_OK) return st;
+  return cuda_status(ttq::launch_remap_pages(table, entries, mapping, num_pages, out, di->err_word, stream));
+}
+
+namespace {
+ttq_status check_logprobs(int64_t rows, int64_t vocab, int64_t top) {
+  if (rows < 1 || rows >= (int64_t(1) << 31) || vocab < 1 || vocab > (int64_t(1) << 20)) return TTQ_ERR_INVALID_ARG;
+  if (top < 0 || top > vocab) return TTQ_ERR_INVALID_ARG;
+  return top > 32 ? TTQ_ERR_UNSUPPORTED : TTQ_OK;
+}
+}  // namespace
+
+ttq_status ttq_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int64_t top, size_t* bytes) {
+  if (!bytes) return TTQ_ERR_INVALID_ARG;
+  const ttq_status st = check_logprobs(rows, vocab, top);
+  if (st != TTQ_OK) return st;
+  *bytes = round256(ttq::token_logprobs_ws_bytes(rows, vocab, top));
+  return TTQ_OK;
+}
+
+ttq_status ttq_token_logprobs(const void* logits, ttq_dtype dtype, int64_t rows, int64_t vocab, int64_t ld,
+                              const int64_t* tokens, int64_t top, float* logprob, float* entropy, int64_t* top_ids,
+                              float* top_logprobs, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!logits || !tokens || !logprob || !entropy) return TTQ_ERR_INVALID_ARG;
+  if (dtype != TTQ_BF16 && dtype != TTQ_FP16 && dtype != TTQ_FP32) return TTQ_ERR_UNSUPPORTED;
+  ttq_status st = check_logprobs(rows, vocab, top);
+  if (st != TTQ_OK) return st;
+  if (ld < vocab || (top > 0) != (top_ids != nullptr) || (top > 0) != (top_logprobs != nullptr) ||
+      logprob == entropy)
+    return TTQ_ERR_INVALID_ARG;
+  const size_t need = ttq::token_logprobs_ws_bytes(rows, vocab, top);
+  if (need > 0 && (!ws || ws_bytes < need)) return TTQ_ERR_WORKSPACE;
+  if (!aligned16(logits) || !aligned8(tokens) || !aligned16(logprob) || !aligned16(entropy) ||
+      (top_ids && !aligned16(top_ids)) || (top_logprobs && !aligned16(top_logprobs)) || (ws && !aligned16(ws)))
+    return TTQ_ERR_MISALIGNED;
+  DeviceInfo* di = nullptr;
+  st = device_info(&di);
+  if (st != TTQ_OK) return st;
+  return cuda_status(ttq::launch_token_logprobs(logits, static_cast<int>(dtype), rows, vocab, ld, tokens, top, logprob,
+                                                entropy, top_ids, top_logprobs, ws, di->num_sms, di->err_word,
+                                                stream));
+}
+
 ttq_status ttq_position_advance(int64_t* pos_dev, int64_t n, cudaStream_t stream) {
   if (!pos_dev || n < 0) return TTQ_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(pos_dev) & 7) return TTQ_ERR_MISALIGNED;

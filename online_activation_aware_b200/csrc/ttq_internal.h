@@ -256,4 +256,41 @@ cudaError_t launch_position_advance(int64_t* pos, int64_t n, cudaStream_t stream
 // out = bf16(silu(gate) * up) over rows of [gate | up] (inter channels each, inter % 8 == 0).
 cudaError_t launch_silu_mul(const void* gu, int64_t rows, int64_t inter, void* out, int num_sms, cudaStream_t stream);
 
+// ---------------------------------------------------------------- paged cache (paged.cu)
+
+// Sizes of a step over a paged cache, and one layer's pools with the page tables.
+struct PagedShape {
+  int64_t seqs, tokens, max_new, heads, kv_heads, head_dim;
+};
+struct PagePool {
+  void* k;
+  void* v;
+  int64_t num_pages, page_size;
+  const int32_t* table;
+  int64_t width;
+};
+
+size_t attention_plan_bytes(int64_t seqs);
+cudaError_t launch_attention_plan(const int32_t* q_start, const int32_t* kv_len, const int32_t* prefix, int64_t window,
+                                  const PagedShape& s, void* plan, unsigned* err, cudaStream_t stream);
+cudaError_t launch_paged_attention(const void* q, int64_t ld_q, const PagedShape& s, const PagePool& p, float softcap,
+                                   const float* slopes, void* out, void* plan, unsigned* err, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope_paged(const void* qkv, const PagedShape& s, const void* wq, const void* wk, float eps,
+                                      const float* rope, int64_t rope_rows, const int32_t* q_start,
+                                      const int32_t* kv_len, const PagePool& p, void* q_out, unsigned* err,
+                                      cudaStream_t stream);
+cudaError_t launch_copy_pages(void* k, void* v, int64_t layers, int64_t num_pages, int64_t page_bytes,
+                              const int32_t* src, const int32_t* dst, int64_t pairs, unsigned* err,
+                              cudaStream_t stream);
+cudaError_t launch_remap_pages(const int32_t* table, int64_t entries, const int32_t* mapping, int64_t num_pages,
+                               int32_t* out, unsigned* err, cudaStream_t stream);
+
+// ---------------------------------------------------------------- token log probabilities (logprobs.cu)
+
+// dtype: 0 bf16, 1 fp16, 2 fp32; top <= 32.
+size_t token_logprobs_ws_bytes(int64_t rows, int64_t vocab, int64_t top);
+cudaError_t launch_token_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                                  const int64_t* tokens, int64_t top, float* logprob, float* entropy, int64_t* top_ids,
+                                  float* top_lp, void* ws, int num_sms, unsigned* err, cudaStream_t stream);
+
 }  // namespace ttq
