@@ -592,7 +592,8 @@ class AttentionPlan:
         n = ctypes.c_size_t(0)
         _check("ttq_attention_plan_size", load_library().ttq_attention_plan_size(
             self.seqs, self.tokens, self.max_new, self.heads, self.kv_heads, self.head_dim, ctypes.byref(n)))
-        self.buffer = torch.zeros(int(n.value), dtype=torch.uint8, device=device)
+        self.buffer = torch.empty(int(n.value), dtype=torch.uint8, device=device)
+        self.buffer[:256].zero_()  # no plan yet
 
     def update(self, q_start, kv_len, window: int = 0, prefix=None, stream=None):
         """Plans a step: sequence b's new tokens are rows q_start[b] .. q_start[b+1] - 1, its

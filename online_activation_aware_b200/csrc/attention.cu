@@ -27,6 +27,7 @@
 #include <cfloat>
 #include <cmath>
 
+#include "attention_common.cuh"
 #include "ttq_internal.h"
 
 namespace ttq {
@@ -77,60 +78,6 @@ struct AttnLayout {
   static constexpr int kMinBlocks = (2 * (kSmem + 1024) <= 228 * 1024 && 2 * kTmemCols <= 512) ? 2 : 1;
 };
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
-                                            int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Shared-memory descriptor of an MN-major operand in the 128-byte-swizzled layout: rows of
-// 64 bf16 (128 B) along MN, 8-row groups along K 1024 B apart (stride byte offset), and the
-// next 64 MN elements one box further on (leading byte offset). Version 1, layout 2.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t lbo_bytes) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>((lbo_bytes >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
-
-// 2^x (the hardware approximation; inputs are <= 0 here, -inf gives 0).
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Waits bounded by a fixed two seconds, ignoring the abort flag: drains copies and products
-// a CTA started before it frees shared and tensor memory.
-__device__ __forceinline__ void attn_drain(uint32_t bar, uint32_t parity, const DevErr& err) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer_ns() - t0 > 2000000000ull) {
-      atomicOr(err.word, kErrTimeout);
-      return;
-    }
-  }
-}
-
 struct AttnArgs {
   int T;            // tokens of the prompt (positions 0 .. T-1)
   int G;            // query heads per key/value head
@@ -140,8 +87,6 @@ struct AttnArgs {
   __nv_bfloat16* out;
   DevErr err;
 };
-
-__device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v ? 1 : 0) != 0; }
 
 template <int D, int BK>
 __global__ void __launch_bounds__(kAttnThreads, AttnLayout<D, BK>::kMinBlocks)

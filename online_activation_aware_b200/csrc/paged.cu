@@ -1,25 +1,10 @@
-// Serving several sequences from a paged key/value cache: the plan of a step's attention, the
-// attention of one or many new tokens per sequence over the pages, the write of new keys and
-// values into pages, and the copies and table rewrites behind forks and compactions.
-//
-// Attention of new token i (of n) of a sequence with L positions, at position p = L - n + i,
-// query head h on key/value head h / G:
-//   s_k = q . k_k / sqrt(D);   s_k <- cap tanh(s_k / cap);   s_k <- s_k + slope_h (k - p);
-//   out = sum_k e^{s_k - m} v_k / sum_k e^{s_k - m}   over the visible k,
-//   visible: k < L and (k < prefix or (k <= p and (window == 0 or k > p - window))).
-#include <algorithm>
-#include <cmath>
-
+// Upkeep of a paged key/value cache: the write of new keys and values into pages, and the page
+// copies and table rewrites behind forks and compactions. (Attention over the pages:
+// paged_attention.cu.)
 #include "ttq_internal.h"
 
 namespace ttq {
 namespace {
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 
 // Sequence of token t: the largest b with start[b] <= t (start[0] = 0, never decreasing).
 __device__ __forceinline__ int find_seq(const int* __restrict__ start, int seqs, int t) {
@@ -29,101 +14,6 @@ __device__ __forceinline__ int find_seq(const int* __restrict__ start, int seqs,
     if (start[mid] <= t) lo = mid; else hi = mid;
   }
   return lo;
-}
-
-// ---------------------------------------------------------------- plan
-
-constexpr unsigned kPlanMagic = 0x54545131u;
-
-// Header of the plan buffer; the lengths follow (start [seqs + 1], len [seqs], prefix [seqs]).
-struct PlanHeader {
-  unsigned magic;  // kPlanMagic when the lengths were in range
-  int seqs, tokens, max_new, heads, kv_heads, head_dim, window;
-};
-
-__global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ q_start, const int* __restrict__ kv_len,
-                                                   const int* __restrict__ prefix, PlanHeader h, int* plan,
-                                                   unsigned* err) {
-  pdl_enter();
-  int* start = plan + sizeof(PlanHeader) / 4;
-  int* len = start + h.seqs + 1;
-  int* pre = len + h.seqs;
-  bool bad = false;
-  for (int b = threadIdx.x; b < h.seqs; b += blockDim.x) {
-    const int s0 = q_start[b], s1 = q_start[b + 1], L = kv_len[b];
-    bad |= (b == 0 && s0 != 0) || s1 < s0 || s1 > h.tokens || s1 - s0 > h.max_new || L < 0 || L > (1 << 30);
-    start[b] = s0;
-    if (b == h.seqs - 1) start[h.seqs] = s1;
-    len[b] = L;
-    pre[b] = prefix ? max(0, min(prefix[b], L)) : 0;
-  }
-  bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0) {
-    h.magic = bad ? 0u : kPlanMagic;
-    *reinterpret_cast<PlanHeader*>(plan) = h;
-    if (bad) atomicOr(err, kErrRange);
-  }
-}
-
-// ---------------------------------------------------------------- attention: one warp per (token, head)
-
-template <int E>
-__global__ void __launch_bounds__(256) paged_attention_simple_kernel(
-    const __nv_bfloat16* __restrict__ q, int64_t ld_q, PlanHeader want, const __nv_bfloat16* __restrict__ kp,
-    const __nv_bfloat16* __restrict__ vp, int num_pages, int page_size, const int* __restrict__ table, int width,
-    float scale, float cap, const float* __restrict__ slopes, __nv_bfloat16* __restrict__ out,
-    const int* __restrict__ plan, unsigned* err) {
-  pdl_enter();
-  constexpr int D = 32 * E;
-  const PlanHeader h = *reinterpret_cast<const PlanHeader*>(plan);
-  if (h.magic != kPlanMagic || h.seqs != want.seqs || h.tokens != want.tokens || h.heads != want.heads ||
-      h.kv_heads != want.kv_heads || h.head_dim != want.head_dim || h.max_new != want.max_new) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(err, kErrRange);
-    return;
-  }
-  const int* start = plan + sizeof(PlanHeader) / 4;
-  const int* len = start + h.seqs + 1;
-  const int* pre = len + h.seqs;
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int t = static_cast<int>(item / h.heads);
-  const int hd = static_cast<int>(item % h.heads);
-  if (t >= start[h.seqs]) return;
-  const int b = find_seq(start, h.seqs, t);
-  const int L = len[b], n = start[b + 1] - start[b], pos = L - n + (t - start[b]);
-  const int kh = hd / (h.heads / h.kv_heads);
-  float qf[E], acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qf[e] = __bfloat162float(q[t * ld_q + hd * D + lane * E + e]) * scale;
-    acc[e] = 0.f;
-  }
-  const float slope = slopes ? slopes[hd] : 0.f;
-  float m = -INFINITY, l = 0.f;
-  for (int k = 0; k < L; ++k) {
-    if (!(k < pre[b] || (k <= pos && (h.window == 0 || k > pos - h.window)))) continue;
-    const int pi = k / page_size;
-    const int page = pi < width ? table[static_cast<int64_t>(b) * width + pi] : -1;
-    if (page < 0 || page >= num_pages) {
-      if (lane == 0) atomicOr(err, kErrRange);
-      break;
-    }
-    const int64_t row = ((static_cast<int64_t>(page) * page_size + k % page_size) * h.kv_heads + kh) * D + lane * E;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(qf[e], __bfloat162float(kp[row + e]), s);
-    s = warp_sum(s);
-    if (cap > 0.f) s = cap * tanhf(s / cap);
-    s += slope * static_cast<float>(k - pos);
-    const float mn = fmaxf(m, s), c = expf(m - mn), w = expf(s - mn);
-    l = l * c + w;
-    m = mn;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * c + w * __bfloat162float(vp[row + e]);
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    out[(static_cast<int64_t>(t) * h.heads + hd) * D + lane * E + e] = __float2bfloat16_rn(l > 0.f ? acc[e] / l : 0.f);
 }
 
 // ---------------------------------------------------------------- new keys and values into pages
@@ -244,40 +134,6 @@ __global__ void __launch_bounds__(256) remap_pages_kernel(const int* table, int6
 }
 
 }  // namespace
-
-size_t attention_plan_bytes(int64_t seqs) { return sizeof(PlanHeader) + (3 * static_cast<size_t>(seqs) + 1) * 4; }
-
-static PlanHeader plan_header(const PagedShape& s, int64_t window) {
-  PlanHeader h = {};
-  h.seqs = static_cast<int>(s.seqs);
-  h.tokens = static_cast<int>(s.tokens);
-  h.max_new = static_cast<int>(s.max_new);
-  h.heads = static_cast<int>(s.heads);
-  h.kv_heads = static_cast<int>(s.kv_heads);
-  h.head_dim = static_cast<int>(s.head_dim);
-  h.window = static_cast<int>(window);
-  return h;
-}
-
-cudaError_t launch_attention_plan(const int32_t* q_start, const int32_t* kv_len, const int32_t* prefix, int64_t window,
-                                  const PagedShape& s, void* plan, unsigned* err, cudaStream_t stream) {
-  return launch_pdl(plan_kernel, dim3(1), dim3(1024), 0, stream, q_start, kv_len, prefix, plan_header(s, window),
-                    static_cast<int*>(plan), err);
-}
-
-cudaError_t launch_paged_attention(const void* q, int64_t ld_q, const PagedShape& s, const PagePool& p, float softcap,
-                                   const float* slopes, void* out, void* plan, unsigned* err, cudaStream_t stream) {
-  const int64_t items = s.tokens * s.heads;
-  const dim3 grid(static_cast<unsigned>((items + 7) / 8));
-  const float scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(s.head_dim)));
-  auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, dim3(256), 0, stream, static_cast<const __nv_bfloat16*>(q), ld_q, plan_header(s, 0),
-                      static_cast<const __nv_bfloat16*>(p.k), static_cast<const __nv_bfloat16*>(p.v),
-                      static_cast<int>(p.num_pages), static_cast<int>(p.page_size), p.table, static_cast<int>(p.width),
-                      scale, softcap, slopes, static_cast<__nv_bfloat16*>(out), static_cast<const int*>(plan), err);
-  };
-  return s.head_dim == 64 ? go(paged_attention_simple_kernel<2>) : go(paged_attention_simple_kernel<4>);
-}
 
 cudaError_t launch_qk_norm_rope_paged(const void* qkv, const PagedShape& s, const void* wq, const void* wk, float eps,
                                       const float* rope, int64_t rope_rows, const int32_t* q_start,

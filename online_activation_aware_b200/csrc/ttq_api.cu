@@ -729,6 +729,15 @@ ttq_status check_pool(const ttq::PagePool& p, int64_t seqs) {
   if (!aligned16(p.k) || !aligned16(p.v) || !aligned16(p.table)) return TTQ_ERR_MISALIGNED;
   return TTQ_OK;
 }
+// SM count of the current device; without one (sizes asked for on the host) the B200's.
+int sms_or_default() {
+  DeviceInfo* di = nullptr;
+  return device_info(&di) == TTQ_OK ? di->num_sms : 148;
+}
+// Blocks of a step: (tiles + split pieces) x kv heads must fit one grid.
+bool grid_fits(const ttq::PagedShape& s) {
+  return (s.tokens + s.seqs + 8192) * s.kv_heads < (int64_t(1) << 31);
+}
 inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 }  // namespace
 
@@ -738,7 +747,8 @@ ttq_status ttq_attention_plan_size(int64_t seqs, int64_t tokens, int64_t max_new
   const ttq::PagedShape s{seqs, tokens, max_new, heads, kv_heads, head_dim};
   const ttq_status st = check_paged(s);
   if (st != TTQ_OK) return st;
-  *bytes = round256(ttq::attention_plan_bytes(seqs));
+  if (!grid_fits(s)) return TTQ_ERR_TOO_LARGE;
+  *bytes = ttq::attention_plan_bytes(s, sms_or_default());
   return TTQ_OK;
 }
 
@@ -749,14 +759,16 @@ ttq_status ttq_attention_plan(const int32_t* q_start, const int32_t* kv_len, con
   const ttq::PagedShape s{seqs, tokens, max_new, heads, kv_heads, head_dim};
   ttq_status st = check_paged(s);
   if (st != TTQ_OK) return st;
+  if (!grid_fits(s)) return TTQ_ERR_TOO_LARGE;
   if (window < 0 || window > (int64_t(1) << 30)) return TTQ_ERR_INVALID_ARG;
-  if (!plan || plan_bytes < ttq::attention_plan_bytes(seqs)) return TTQ_ERR_WORKSPACE;
+  if (!plan || plan_bytes < ttq::attention_plan_bytes(s, sms_or_default())) return TTQ_ERR_WORKSPACE;
   if (!aligned16(q_start) || !aligned16(kv_len) || (prefix && !aligned16(prefix)) || !aligned16(plan))
     return TTQ_ERR_MISALIGNED;
   DeviceInfo* di = nullptr;
   st = device_info(&di);
   if (st != TTQ_OK) return st;
-  return cuda_status(ttq::launch_attention_plan(q_start, kv_len, prefix, window, s, plan, di->err_word, stream));
+  return cuda_status(ttq::launch_attention_plan(q_start, kv_len, prefix, window, s, plan, di->num_sms, di->err_word,
+                                                stream));
 }
 
 ttq_status ttq_paged_attention(const void* q_bf16, int64_t ld_q, int64_t seqs, int64_t tokens, int64_t max_new,
@@ -774,15 +786,16 @@ ttq_status ttq_paged_attention(const void* q_bf16, int64_t ld_q, int64_t seqs, i
   if (st != TTQ_OK) return st;
   if (ld_q < heads * head_dim || ld_q > (int64_t(1) << 30)) return TTQ_ERR_INVALID_ARG;
   if (!std::isfinite(softcap) || softcap < 0.f) return TTQ_ERR_INVALID_ARG;
-  if (!plan || plan_bytes < ttq::attention_plan_bytes(seqs)) return TTQ_ERR_WORKSPACE;
+  if (!grid_fits(s)) return TTQ_ERR_TOO_LARGE;
+  if (!plan || plan_bytes < ttq::attention_plan_bytes(s, sms_or_default())) return TTQ_ERR_WORKSPACE;
   if (!aligned16(q_bf16) || ld_q % 8 != 0 || !aligned16(out_bf16) || !aligned16(plan) ||
       (slopes && !aligned16(slopes)))
     return TTQ_ERR_MISALIGNED;
   DeviceInfo* di = nullptr;
   st = device_info(&di);
   if (st != TTQ_OK) return st;
-  return cuda_status(ttq::launch_paged_attention(q_bf16, ld_q, s, p, softcap, slopes, out_bf16, plan, di->err_word,
-                                                 stream));
+  return cuda_status(ttq::launch_paged_attention(q_bf16, ld_q, s, p, softcap, slopes, out_bf16, plan, di->num_sms,
+                                                 dev_err(di), stream));
 }
 
 ttq_status ttq_qk_norm_rope_paged(const void* qkv_bf16, int64_t seqs, int64_t tokens, int64_t heads, int64_t kv_heads,

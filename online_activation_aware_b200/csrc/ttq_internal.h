@@ -256,7 +256,7 @@ cudaError_t launch_position_advance(int64_t* pos, int64_t n, cudaStream_t stream
 // out = bf16(silu(gate) * up) over rows of [gate | up] (inter channels each, inter % 8 == 0).
 cudaError_t launch_silu_mul(const void* gu, int64_t rows, int64_t inter, void* out, int num_sms, cudaStream_t stream);
 
-// ---------------------------------------------------------------- paged cache (paged.cu)
+// ---------------------------------------------------------------- paged cache (paged_attention.cu, paged.cu)
 
 // Sizes of a step over a paged cache, and one layer's pools with the page tables.
 struct PagedShape {
@@ -270,11 +270,12 @@ struct PagePool {
   int64_t width;
 };
 
-size_t attention_plan_bytes(int64_t seqs);
+size_t attention_plan_bytes(const PagedShape& s, int num_sms);
 cudaError_t launch_attention_plan(const int32_t* q_start, const int32_t* kv_len, const int32_t* prefix, int64_t window,
-                                  const PagedShape& s, void* plan, unsigned* err, cudaStream_t stream);
+                                  const PagedShape& s, void* plan, int num_sms, unsigned* err, cudaStream_t stream);
 cudaError_t launch_paged_attention(const void* q, int64_t ld_q, const PagedShape& s, const PagePool& p, float softcap,
-                                   const float* slopes, void* out, void* plan, unsigned* err, cudaStream_t stream);
+                                   const float* slopes, void* out, void* plan, int num_sms, const DevErr& err,
+                                   cudaStream_t stream);
 cudaError_t launch_qk_norm_rope_paged(const void* qkv, const PagedShape& s, const void* wq, const void* wk, float eps,
                                       const float* rope, int64_t rope_rows, const int32_t* q_start,
                                       const int32_t* kv_len, const PagePool& p, void* q_out, unsigned* err,

@@ -260,7 +260,7 @@ def test_bad_lengths_and_pages_are_reported():
         assert ttq.device_status() == INVALID
     # a plan of other sizes
     p = ttq.AttentionPlan(2, c.N, 8, 2, 64).update(c.start, c.ld)
-    p.max_new = 2
+    p.max_new = 5
     ttq.paged_attention(c.qd, p, c.kd, c.vd, c.td, out=out)
     assert ttq.device_status() == INVALID
     # lengths past the table, and entries that are no pages
