@@ -542,35 +542,71 @@ def silu_mul(gate_up, out=None, stream=None):
 # ------------------------------------------------------------------ paged cache, several sequences
 
 
-def _device_of(**tensors):
-    """The CUDA device all the given tensors (None skipped) are on."""
+class _OnDevice:
+    """Makes a device current for a call and restores the caller's (entered only when they differ)."""
+
+    __slots__ = ("index", "guard")
+
+    def __init__(self, index: int):
+        self.index, self.guard = index, None
+
+    def __enter__(self):
+        import torch
+
+        if torch.cuda.current_device() != self.index:
+            self.guard = torch.cuda.device(self.index)
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _same_device(*named):
+    """Guard for the one CUDA device that all the given (name, tensor) pairs are on (None skipped)."""
     import torch
 
-    dev = None
-    for name, t in tensors.items():
+    index = None
+    for name, t in named:
         if t is None:
             continue
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
-    return torch.cuda.device(dev)
+        at = t.get_device()
+        if index is None:
+            index = at
+        elif at != index:
+            raise ValueError(f"{name} is on cuda:{at}, the other tensors on cuda:{index}")
+    return _OnDevice(index)
 
 
-def _shape(t, name, *dims):
-    """Raises unless t has the given sizes (None: any)."""
-    if t is not None and (t.dim() != len(dims) or any(d is not None and d != n for d, n in zip(dims, t.shape))):
+def _address(t, dtype, name):
+    """Address of a contiguous tensor of the given type (None -> NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _shape(t, name, dims):
+    """Raises unless t (None skipped) has the given sizes."""
+    if t is not None and tuple(t.shape) != dims:
         raise ValueError(f"{name} must have shape {list(dims)}, got {list(t.shape)}")
 
 
 def _pool(k_pages, v_pages, page_table, seqs: int, kv_heads: int, head_dim: int):
-    _shape(k_pages, "k_pages", None, None, kv_heads, head_dim)
-    _shape(v_pages, "v_pages", *k_pages.shape)
-    _shape(page_table, "page_table", seqs, None)
+    shape = tuple(k_pages.shape)
+    if len(shape) != 4 or shape[2:] != (kv_heads, head_dim):
+        raise ValueError(f"k_pages must have shape [pages, page_size, {kv_heads}, {head_dim}], got {list(shape)}")
+    _shape(v_pages, "v_pages", shape)
+    if page_table.dim() != 2 or page_table.shape[0] != seqs:
+        raise ValueError(f"page_table must have shape [{seqs}, width], got {list(page_table.shape)}")
+    return shape[0], shape[1], page_table.shape[1]
 
 
 class AttentionPlan:
@@ -599,16 +635,16 @@ class AttentionPlan:
         """Plans a step: sequence b's new tokens are rows q_start[b] .. q_start[b+1] - 1, its
         cache holds kv_len[b] positions with them (int32 tensors). ``window`` > 0 limits every
         token to that many positions; the first prefix[b] positions stay visible to all."""
-        import torch
+        from torch import int32
 
-        _shape(q_start, "q_start", self.seqs + 1)
-        _shape(kv_len, "kv_len", self.seqs)
-        _shape(prefix, "prefix", self.seqs)
-        with _device_of(q_start=q_start, kv_len=kv_len, prefix=prefix, plan=self.buffer):
+        _shape(q_start, "q_start", (self.seqs + 1,))
+        _shape(kv_len, "kv_len", (self.seqs,))
+        _shape(prefix, "prefix", (self.seqs,))
+        with _same_device(("q_start", q_start), ("kv_len", kv_len), ("prefix", prefix), ("plan", self.buffer)):
             _check("ttq_attention_plan", load_library().ttq_attention_plan(
-                _ptr(q_start, torch.int32, "q_start"), _ptr(kv_len, torch.int32, "kv_len"),
-                _ptr(prefix, torch.int32, "prefix"), window, self.seqs, self.tokens, self.max_new, self.heads,
-                self.kv_heads, self.head_dim, _ptr(self.buffer), self.buffer.numel(), _stream(stream)))
+                _address(q_start, int32, "q_start"), _address(kv_len, int32, "kv_len"),
+                _address(prefix, int32, "prefix"), window, self.seqs, self.tokens, self.max_new, self.heads,
+                self.kv_heads, self.head_dim, self.buffer.data_ptr(), self.buffer.numel(), _stream(stream)))
         return self
 
 
@@ -619,28 +655,25 @@ def paged_attention(q, plan: AttentionPlan, k_pages, v_pages, page_table, softca
     [num_pages, page_size, kv_heads, head_dim] bf16, page_table [seqs, width] int32. Scores are
     capped to softcap * tanh(s / softcap) when softcap > 0, then biased by slopes[h] * (k - pos).
     Returns out [tokens, heads * head_dim] bf16; rows past the last sequence are not written."""
-    import torch
+    from torch import bfloat16, float32, int32
 
-    H, D = plan.heads, plan.head_dim
-    _pool(k_pages, v_pages, page_table, plan.seqs, plan.kv_heads, D)
-    _shape(slopes, "slopes", H)
-    _shape(q, "q", plan.tokens, None)
-    if q.shape[1] < H * D or q.stride(1) != 1:
-        raise ValueError(f"q must have at least {H * D} contiguous channels a row")
-    _shape(out, "out", plan.tokens, H * D)
-    with _device_of(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, slopes=slopes, out=out,
-                    plan=plan.buffer):
-        if q.dtype != torch.bfloat16:
-            raise TypeError(f"q must be {torch.bfloat16}, got {q.dtype}")
+    H, D, T = plan.heads, plan.head_dim, plan.tokens
+    pages, page_size, width = _pool(k_pages, v_pages, page_table, plan.seqs, plan.kv_heads, D)
+    _shape(slopes, "slopes", (H,))
+    _shape(out, "out", (T, H * D))
+    if q.dim() != 2 or q.shape[0] != T or q.shape[1] < H * D or q.stride(1) != 1:
+        raise ValueError(f"q must be {T} rows of at least {H * D} contiguous channels, got {list(q.shape)}")
+    if q.dtype != bfloat16:
+        raise TypeError(f"q must be {bfloat16}, got {q.dtype}")
+    with _same_device(("q", q), ("k_pages", k_pages), ("v_pages", v_pages), ("page_table", page_table),
+                      ("slopes", slopes), ("out", out), ("plan", plan.buffer)):
         if out is None:
-            out = torch.empty(plan.tokens, H * D, dtype=torch.bfloat16, device=q.device)
-        ld = q.stride(0) if plan.tokens > 1 else max(q.stride(0), H * D)
+            out = q.new_empty((T, H * D))
         _check("ttq_paged_attention", load_library().ttq_paged_attention(
-            ctypes.c_void_p(q.data_ptr()), ld, plan.seqs, plan.tokens, plan.max_new, H, plan.kv_heads, D,
-            _ptr(k_pages, torch.bfloat16, "k_pages"), _ptr(v_pages, torch.bfloat16, "v_pages"), k_pages.shape[0],
-            k_pages.shape[1], _ptr(page_table, torch.int32, "page_table"), page_table.shape[1], softcap,
-            _ptr(slopes, torch.float32, "slopes"), _ptr(out, torch.bfloat16, "out"), _ptr(plan.buffer),
-            plan.buffer.numel(), _stream(stream)))
+            q.data_ptr(), q.stride(0) if T > 1 else q.shape[1], plan.seqs, T, plan.max_new, H, plan.kv_heads, D,
+            _address(k_pages, bfloat16, "k_pages"), _address(v_pages, bfloat16, "v_pages"), pages, page_size,
+            _address(page_table, int32, "page_table"), width, softcap, _address(slopes, float32, "slopes"),
+            _address(out, bfloat16, "out"), plan.buffer.data_ptr(), plan.buffer.numel(), _stream(stream)))
     return out
 
 
@@ -650,28 +683,29 @@ def qk_norm_rope_paged(qkv, heads: int, kv_heads: int, head_dim: int, q_norm, k_
     written to their sequences' pages at positions kv_len[b] - n .. kv_len[b] - 1, and the
     normalised, rotated q heads to q [tokens, heads * head_dim], which is returned (qkv is only
     read; rows past the last sequence are not written)."""
-    import torch
+    from torch import bfloat16, float32, int32
 
     T = qkv.shape[0]
     seqs = kv_len.shape[0]
-    _shape(qkv, "qkv", None, (heads + 2 * kv_heads) * head_dim)
-    _pool(k_pages, v_pages, page_table, seqs, kv_heads, head_dim)
-    _shape(q_start, "q_start", seqs + 1)
-    _shape(q_norm, "q_norm", head_dim)
-    _shape(k_norm, "k_norm", head_dim)
-    _shape(table, "table", None, head_dim // 2, 2)
-    _shape(q, "q", T, heads * head_dim)
-    with _device_of(qkv=qkv, q_norm=q_norm, k_norm=k_norm, table=table, q_start=q_start, kv_len=kv_len, k_pages=k_pages,
-                    v_pages=v_pages, page_table=page_table, q=q):
+    _shape(qkv, "qkv", (T, (heads + 2 * kv_heads) * head_dim))
+    pages, page_size, width = _pool(k_pages, v_pages, page_table, seqs, kv_heads, head_dim)
+    _shape(q_start, "q_start", (seqs + 1,))
+    _shape(kv_len, "kv_len", (seqs,))
+    _shape(q_norm, "q_norm", (head_dim,))
+    _shape(k_norm, "k_norm", (head_dim,))
+    _shape(table, "table", (table.shape[0], head_dim // 2, 2))
+    _shape(q, "q", (T, heads * head_dim))
+    with _same_device(("qkv", qkv), ("q_norm", q_norm), ("k_norm", k_norm), ("table", table), ("q_start", q_start),
+                      ("kv_len", kv_len), ("k_pages", k_pages), ("v_pages", v_pages), ("page_table", page_table),
+                      ("q", q)):
         if q is None:
-            q = torch.empty(T, heads * head_dim, dtype=torch.bfloat16, device=qkv.device)
+            q = qkv.new_empty((T, heads * head_dim))
         _check("ttq_qk_norm_rope_paged", load_library().ttq_qk_norm_rope_paged(
-            _ptr(qkv, torch.bfloat16, "qkv"), seqs, T, heads, kv_heads, head_dim, _ptr(q_norm, torch.bfloat16, "q_norm"),
-            _ptr(k_norm, torch.bfloat16, "k_norm"), eps, _ptr(table, torch.float32, "table"), table.shape[0],
-            _ptr(q_start, torch.int32, "q_start"), _ptr(kv_len, torch.int32, "kv_len"),
-            _ptr(k_pages, torch.bfloat16, "k_pages"), _ptr(v_pages, torch.bfloat16, "v_pages"), k_pages.shape[0],
-            k_pages.shape[1], _ptr(page_table, torch.int32, "page_table"), page_table.shape[1],
-            _ptr(q, torch.bfloat16, "q"), _stream(stream)))
+            _address(qkv, bfloat16, "qkv"), seqs, T, heads, kv_heads, head_dim, _address(q_norm, bfloat16, "q_norm"),
+            _address(k_norm, bfloat16, "k_norm"), eps, _address(table, float32, "table"), table.shape[0],
+            _address(q_start, int32, "q_start"), _address(kv_len, int32, "kv_len"),
+            _address(k_pages, bfloat16, "k_pages"), _address(v_pages, bfloat16, "v_pages"), pages, page_size,
+            _address(page_table, int32, "page_table"), width, _address(q, bfloat16, "q"), _stream(stream)))
     return q
 
 
@@ -680,37 +714,39 @@ def copy_pages(k_pool, v_pool, src, dst, stream=None):
     [num_pages, page_size, kv_heads, head_dim] or [layers, num_pages, ...], of one type; src and
     dst int32 tensors on the pools' device. Every destination appears once and is no source of
     another pair."""
-    import torch
+    from torch import int32
 
-    if k_pool.dim() not in (4, 5):
+    shape = tuple(k_pool.shape)
+    if len(shape) not in (4, 5):
         raise ValueError("pools are [num_pages, page_size, kv_heads, head_dim], with the layers ahead or without")
-    _shape(v_pool, "v_pool", *k_pool.shape)
-    layers = k_pool.shape[0] if k_pool.dim() == 5 else 1
-    pages = k_pool.shape[-4]
-    page_bytes = k_pool[..., 0, :, :, :].numel() // layers * k_pool.element_size()
-    _shape(src, "src", None)
-    _shape(dst, "dst", *src.shape)
-    if src.numel() == 0:
-        return
-    with _device_of(k_pool=k_pool, v_pool=v_pool, src=src, dst=dst):
+    _shape(v_pool, "v_pool", shape)
+    if src.dim() != 1:
+        raise ValueError("src and dst are lists of pages")
+    _shape(dst, "dst", tuple(src.shape))
+    layers = shape[0] if len(shape) == 5 else 1
+    page_bytes = shape[-3] * shape[-2] * shape[-1] * k_pool.element_size()
+    with _same_device(("k_pool", k_pool), ("v_pool", v_pool), ("src", src), ("dst", dst)):
+        if src.shape[0] == 0:
+            return
         _check("ttq_copy_pages", load_library().ttq_copy_pages(
-            _ptr(k_pool, None, "k_pool"), _ptr(v_pool, k_pool.dtype, "v_pool"), layers, pages, page_bytes,
-            _ptr(src, torch.int32, "src"), _ptr(dst, torch.int32, "dst"), src.numel(), _stream(stream)))
+            _address(k_pool, k_pool.dtype, "k_pool"), _address(v_pool, k_pool.dtype, "v_pool"), layers, shape[-4],
+            page_bytes, _address(src, int32, "src"), _address(dst, int32, "dst"), src.shape[0], _stream(stream)))
 
 
 def remap_pages(table, mapping, out=None, stream=None):
     """Page tables after their pages moved: out = mapping[table] for entries that are pages,
     negative entries as they are (int32 tensors; ``out`` may be ``table``)."""
-    import torch
+    from torch import int32
 
-    _shape(mapping, "mapping", None)
-    with _device_of(table=table, mapping=mapping, out=out):
+    if mapping.dim() != 1:
+        raise ValueError("mapping holds one entry a page")
+    _shape(out, "out", tuple(table.shape))
+    with _same_device(("table", table), ("mapping", mapping), ("out", out)):
         if out is None:
-            out = torch.empty_like(table)
-        _shape(out, "out", *table.shape)
+            out = table.new_empty(table.shape)
         _check("ttq_remap_pages", load_library().ttq_remap_pages(
-            _ptr(table, torch.int32, "table"), table.numel(), _ptr(mapping, torch.int32, "mapping"), mapping.numel(),
-            _ptr(out, torch.int32, "out"), _stream(stream)))
+            _address(table, int32, "table"), table.numel(), _address(mapping, int32, "mapping"), mapping.shape[0],
+            _address(out, int32, "out"), _stream(stream)))
     return out
 
 
@@ -722,29 +758,30 @@ def token_logprobs(logits, tokens, top: int = 0, ws=None, stream=None):
     order, equal logits by rising index."""
     import torch
 
-    _shape(logits, "logits", None, None)
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be rows of contiguous logits")
     rows, vocab = logits.shape
-    _shape(tokens, "tokens", rows)
-    if logits.stride(1) != 1 and vocab > 1:
-        raise ValueError("a row's logits must be contiguous")
-    kinds = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-    if logits.dtype not in kinds:
+    _shape(tokens, "tokens", (rows,))
+    kind = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(logits.dtype)
+    if kind is None:
         raise TypeError(f"logits must be bf16, fp16 or fp32, got {logits.dtype}")
-    with _device_of(logits=logits, tokens=tokens, ws=ws):
-        dev = logits.device
+    with _same_device(("logits", logits), ("tokens", tokens), ("ws", ws)):
+        lib = load_library()
         n = ctypes.c_size_t(0)
-        _check("ttq_token_logprobs_workspace_size", load_library().ttq_token_logprobs_workspace_size(
-            rows, vocab, top, ctypes.byref(n)))
+        _check("ttq_token_logprobs_workspace_size",
+               lib.ttq_token_logprobs_workspace_size(rows, vocab, top, ctypes.byref(n)))
         if ws is None and n.value > 0:
-            ws = torch.empty(int(n.value), dtype=torch.uint8, device=dev)
-        out = {"logprob": torch.empty(rows, dtype=torch.float32, device=dev),
-               "entropy": torch.empty(rows, dtype=torch.float32, device=dev)}
+            ws = logits.new_empty(n.value, dtype=torch.uint8)
+        out = {"logprob": logits.new_empty(rows, dtype=torch.float32),
+               "entropy": logits.new_empty(rows, dtype=torch.float32)}
+        ids = lps = None
         if top > 0:
-            out["top_ids"] = torch.empty(rows, top, dtype=torch.int64, device=dev)
-            out["top_logprobs"] = torch.empty(rows, top, dtype=torch.float32, device=dev)
-        _check("ttq_token_logprobs", load_library().ttq_token_logprobs(
-            ctypes.c_void_p(logits.data_ptr()), kinds[logits.dtype], rows, vocab,
-            logits.stride(0) if rows > 1 else max(logits.stride(0), vocab), _ptr(tokens, torch.int64, "tokens"), top,
-            _ptr(out["logprob"]), _ptr(out["entropy"]), _ptr(out.get("top_ids")), _ptr(out.get("top_logprobs")),
-            _ptr(ws, None, "ws"), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+            ids = out["top_ids"] = logits.new_empty((rows, top), dtype=torch.int64)
+            lps = out["top_logprobs"] = logits.new_empty((rows, top), dtype=torch.float32)
+        _check("ttq_token_logprobs", lib.ttq_token_logprobs(
+            logits.data_ptr(), kind, rows, vocab, logits.stride(0) if rows > 1 else vocab,
+            _address(tokens, torch.int64, "tokens"), top, out["logprob"].data_ptr(), out["entropy"].data_ptr(),
+            None if ids is None else ids.data_ptr(), None if lps is None else lps.data_ptr(),
+            None if ws is None else _address(ws, ws.dtype, "ws"), 0 if ws is None else ws.numel() * ws.element_size(),
+            _stream(stream)))
     return out

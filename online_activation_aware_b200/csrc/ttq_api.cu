@@ -866,7 +866,7 @@ ttq_status ttq_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int64_
   if (!bytes) return TTQ_ERR_INVALID_ARG;
   const ttq_status st = check_logprobs(rows, vocab, top);
   if (st != TTQ_OK) return st;
-  *bytes = round256(ttq::token_logprobs_ws_bytes(rows, vocab, top));
+  *bytes = round256(ttq::token_logprobs_ws_bytes(rows, vocab, top, sms_or_default()));
   return TTQ_OK;
 }
 
@@ -880,7 +880,7 @@ ttq_status ttq_token_logprobs(const void* logits, ttq_dtype dtype, int64_t rows,
   if (ld < vocab || (top > 0) != (top_ids != nullptr) || (top > 0) != (top_logprobs != nullptr) ||
       logprob == entropy)
     return TTQ_ERR_INVALID_ARG;
-  const size_t need = ttq::token_logprobs_ws_bytes(rows, vocab, top);
+  const size_t need = ttq::token_logprobs_ws_bytes(rows, vocab, top, sms_or_default());
   if (need > 0 && (!ws || ws_bytes < need)) return TTQ_ERR_WORKSPACE;
   if (!aligned16(logits) || !aligned8(tokens) || !aligned16(logprob) || !aligned16(entropy) ||
       (top_ids && !aligned16(top_ids)) || (top_logprobs && !aligned16(top_logprobs)) || (ws && !aligned16(ws)))
