@@ -6,10 +6,12 @@
 // to base 2, so that logits at the type's lowest value (masks) cannot overflow.
 //
 // The alternatives come out of the same pass. A logit's key is (order of its value, lowest index
-// first) in 64 bits, so no two are equal; only keys above a threshold are put into a shared
-// candidate list. The threshold starts as the top-th largest of the threads' maxima in the
-// first chunk (at least `top` logits are that large) and rises whenever the list is cut back to
-// its `top` best; a chunk whose maximum is below it costs one comparison a thread.
+// first) in 64 bits, so no two are equal. Every warp keeps its best keys sorted, one a lane, and
+// inserts a key with two shuffles; only keys above a threshold get that far: the top-th best key
+// of the block so far. It starts from the lanes' best keys of the first chunk, sorted and merged
+// over the block, and is renewed after 2, 4, 8, ... chunks, when the warps hand their lists to the
+// first one (a merge of two sorted lists of 32 is six shuffles), so that about 5 `top` keys a row
+// are ever inserted. A chunk whose maximum is below the threshold costs one comparison a thread.
 //
 // Memory bound: one read of the logits. Few rows are split over several blocks (segments), whose
 // sums and candidates a second kernel joins.
@@ -23,38 +25,92 @@
 namespace ttq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kVecs = 4;         // 16-byte vectors a thread takes per chunk
-constexpr int kList = 1024;      // capacity of the candidate list
-constexpr int kCut = 256;        // cut it back to `top` past this many
-constexpr int kMaxTop = 32;
+constexpr int kStages = 3;       // chunks in flight, the one at work included
+constexpr int kWarps = kThreads / 32;
+constexpr int kChunk = kVecs * kThreads;  // vectors of a chunk
+constexpr int kMaxTop = 32;      // one key a lane
 constexpr int kMaxSegments = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// A 16-byte vector of N logits: pair i as two floats, and the largest of kVecs vectors (a NaN is
+// passed over; of nothing but NaN it is -inf or NaN).
 template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ float get(const uint4& v, int i) {
-    return __uint_as_float(reinterpret_cast<const uint32_t*>(&v)[i]);
+  static constexpr uint32_t kNone = 0xff800000u;  // -inf
+  static __device__ __forceinline__ float2 pair(const uint4& v, int i) { return reinterpret_cast<const float2*>(&v)[i]; }
+  static __device__ __forceinline__ float largest(const uint4 (&w)[kVecs]) {
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m[u] = fmaxf(m[u], reinterpret_cast<const float*>(&w[u])[i]);
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
   }
 };
+template <typename H2>
+__device__ __forceinline__ H2 largest_pair(const uint4 (&w)[kVecs]) {
+  H2 m[kVecs];
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    const H2* h = reinterpret_cast<const H2*>(&w[u]);
+    m[u] = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+  }
+  return __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+}
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ float get(const uint4& v, int i) {
-    const uint32_t w = reinterpret_cast<const uint32_t*>(&v)[i >> 1];
-    return (i & 1) ? bf16hi_to_f32(w) : bf16lo_to_f32(w);
+  static constexpr uint32_t kNone = 0xff80ff80u;
+  static __device__ __forceinline__ float2 pair(const uint4& v, int i) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(&v)[i];
+    return make_float2(bf16lo_to_f32(w), bf16hi_to_f32(w));
+  }
+  static __device__ __forceinline__ float largest(const uint4 (&w)[kVecs]) {
+    const __nv_bfloat162 m = largest_pair<__nv_bfloat162>(w);
+    return fmaxf(__low2float(m), __high2float(m));
   }
 };
 template <>
 struct Vec<__half> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ float get(const uint4& v, int i) {
-    return __half2float(reinterpret_cast<const __half*>(&v)[i]);
+  static constexpr uint32_t kNone = 0xfc00fc00u;
+  static __device__ __forceinline__ float2 pair(const uint4& v, int i) {
+    return __half22float2(reinterpret_cast<const __half2*>(&v)[i]);
+  }
+  static __device__ __forceinline__ float largest(const uint4 (&w)[kVecs]) {
+    const __half2 m = largest_pair<__half2>(w);
+    return fmaxf(__low2float(m), __high2float(m));
   }
 };
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
+  return a;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
+  return a;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+  return c;
+}
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -119,20 +175,45 @@ __device__ __forceinline__ void write_row(const Outs& o, int64_t r, const Sums& 
   o.entropy[r] = ls - a.t / a.s;
 }
 
-// Rank of every key of list[0 .. n): the largest has rank 0. f(rank, key) is called for each.
-template <typename F>
-__device__ __forceinline__ void for_ranks(const unsigned long long* list, int n, F f) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const unsigned long long k = list[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += list[j] > k;
-    f(rank, k);
-  }
+using Key = unsigned long long;
+
+__device__ __forceinline__ Key exchange(Key a, int o, bool keep_max) {
+  const Key b = __shfl_xor_sync(0xffffffffu, a, o);
+  return keep_max == (a > b) ? a : b;
+}
+// The warp's keys in falling order, one a lane.
+__device__ __forceinline__ Key sort_keys(Key a) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+    for (int o = k >> 1; o > 0; o >>= 1) a = exchange(a, o, ((lane & o) == 0) == ((lane & k) == 0));
+  return a;
+}
+// The 32 best of two falling lists, in falling order.
+__device__ __forceinline__ Key merge_keys(Key a, Key b) {
+  const int lane = threadIdx.x & 31;
+  a = max(a, __shfl_xor_sync(0xffffffffu, b, 31));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a = exchange(a, o, (lane & o) == 0);
+  return a;
+}
+
+// The 32 best of kWarps falling lists, in falling order (pairs first: their steps overlap).
+__device__ __forceinline__ Key merge_lists(const Key (&lists)[kWarps][32]) {
+  Key k[kWarps];
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) k[i] = lists[i][threadIdx.x & 31];
+#pragma unroll
+  for (int n = kWarps / 2; n > 0; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) k[i] = merge_keys(k[i], k[i + n]);
+  return k[0];
 }
 
 // The block's sums, in every thread.
 __device__ __forceinline__ Sums block_join(Sums a) {
-  __shared__ Sums sh[kThreads / 32];
+  __shared__ Sums sh[kWarps];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     Sums b;
@@ -145,25 +226,25 @@ __device__ __forceinline__ Sums block_join(Sums a) {
   __syncthreads();
   a = sh[0];
 #pragma unroll
-  for (int w = 1; w < kThreads / 32; ++w) a = join(a, sh[w]);
+  for (int w = 1; w < kWarps; ++w) a = join(a, sh[w]);
   return a;
 }
 
-// Partial results of a segment: its sums, the number of its candidates and their keys.
-struct Part {
-  Sums a;
-  int n;
-};
+// The alternative of rank threadIdx.x.
+__device__ __forceinline__ void write_top(const Outs& o, int64_t r, int top, const Sums& a, Key k) {
+  o.top_ids[r * top + threadIdx.x] = key_index(k);
+  o.top_lp[r * top + threadIdx.x] = (key_value(static_cast<unsigned>(k >> 32)) - a.m) - log_sum(a);
+}
 
 // One block per (row, segment). ONE: the row's only segment.
 template <typename T, bool TOP, bool ONE>
-__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const T* __restrict__ logits, int vocab, int64_t ld,
-                                                                    int segments, int top, Outs o, Part* parts,
-                                                                    unsigned long long* part_keys) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kernel(const T* __restrict__ logits, int vocab, int64_t ld,
+                                                                    int segments, int top, Outs o, Sums* parts,
+                                                                    Key* part_keys) {
   constexpr int N = Vec<T>::N;
-  __shared__ unsigned long long list[TOP ? kList : 1], kept[kMaxTop];
-  __shared__ unsigned long long tau_sh;
-  __shared__ int count;
+  __shared__ Key lists[2][kWarps][32];  // the warps' lists, by turns
+  extern __shared__ uint4 ring[];          // [kStages][kVecs][kThreads]
+  __shared__ Key tau_sh;  // a key that at least `top` of the block's reach
   pdl_enter();
   const int tid = threadIdx.x;
   const int64_t r = ONE ? blockIdx.x : blockIdx.x / segments;
@@ -175,155 +256,144 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const T* __
   const int nv = (head + vocab + N - 1) / N;
   const int v0 = static_cast<int>(static_cast<int64_t>(nv) * seg / segments);
   const int v1 = static_cast<int>(static_cast<int64_t>(nv) * (seg + 1) / segments);
-  const uint32_t none = sizeof(T) == 4 ? 0xff800000u : (std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u);
-  const uint4 nothing = make_uint4(none, none, none, none);  // -inf everywhere
+  const uint32_t none = Vec<T>::kNone;
+  const uint4 nothing = make_uint4(none, none, none, none);
 
-  auto load = [&](int v) -> uint4 {
-    if (v >= v1) return nothing;
-    if (v > 0 ? (v + 1) * N <= head + vocab : (head == 0 && N <= vocab)) return __ldcs(xv + v);
-    // first or last vector: only the row's own elements
-    uint4 w = nothing;
-    T* e = reinterpret_cast<T*>(&w);
-#pragma unroll
+  // vector v into this thread's place of the ring (each thread reads back its own: no barrier)
+  auto fetch = [&](int v, uint4* to) {
+    if (v < v1 && (v > 0 ? (v + 1) * N <= head + vocab : (head == 0 && N <= vocab))) {
+      cp_async_16(smem_addr(to), xv + v);
+      return;
+    }
+    // past the end, or the row's first or last vector: only the row's own elements
+    *to = nothing;
+    if (v >= v1) return;
+    T* e = reinterpret_cast<T*>(to);
     for (int i = 0; i < N; ++i) {
       const int k = v * N + i - head;
       if (k >= 0 && k < vocab) e[i] = x[k];
     }
-    return w;
   };
 
-  if (TOP) {
-    if (tid == 0) count = 0;
-    __syncthreads();
-  }
+  const int lane = tid & 31, warp = tid >> 5;
   Sums a = {-INFINITY, 0.f, 0.f};
-  unsigned long long tau = 0;
-  float tau_x = 0.f;
-  uint4 w[kVecs], nx[kVecs];
-#pragma unroll
-  for (int u = 0; u < kVecs; ++u) nx[u] = load(v0 + u * kThreads + tid);
-  for (int c = v0; c < v1; c += kVecs * kThreads) {
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) w[u] = nx[u];
-    if (c + kVecs * kThreads < v1) {
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u) nx[u] = load(c + (kVecs + u) * kThreads + tid);
+  Key mine = 0;   // the warp's key of rank `lane`
+  Key floor = 0;  // keys at or below it are not among the best
+  int turn = 0;
+  // every warp's list to the first, which publishes the threshold
+  auto gather = [&]() {
+    lists[turn][warp][lane] = mine;
+    __syncthreads();
+    if (warp == 0) {
+      mine = merge_lists(lists[turn]);
+      if (lane == top - 1) *const_cast<volatile Key*>(&tau_sh) = mine;
+    } else {
+      mine = 0;
     }
-    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    turn ^= 1;
+  };
+  const int chunks = (v1 - v0 + kChunk - 1) / kChunk;
+  auto fetch_chunk = [&](int i) {
+    if (i < chunks) {
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u)
+      for (int u = 0; u < kVecs; ++u)
+        fetch(v0 + i * kChunk + u * kThreads + tid, ring + ((i % kStages) * kVecs + u) * kThreads + tid);
+    }
+    cp_async_commit();
+  };
 #pragma unroll
-      for (int i = 0; i < N; ++i) mx[i & 3] = fmaxf(mx[i & 3], Vec<T>::get(w[u], i));
-    const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  for (int i = 0; i < kStages - 1; ++i) fetch_chunk(i);
+#pragma unroll 1
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    const int c = v0 + chunk * kChunk;
+    if (TOP) __syncwarp();  // the warp is done with the chunk whose place is filled next
+    fetch_chunk(chunk + kStages - 1);
+    cp_async_wait<kStages - 1>();
+    const uint4* here = ring + (chunk % kStages) * kVecs * kThreads;
+    uint4 w[kVecs];
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) w[u] = here[u * kThreads + tid];
+    const float bm = Vec<T>::largest(w);
     if (bm > a.m) raise(a, bm);
     const float ref = reference(a.m);
-    float s2[2] = {0.f, 0.f}, t2[2] = {0.f, 0.f};
+    const uint64_t ref2 = pack2(-ref, -ref), scale2 = pack2(kLog2e, kLog2e);
+    uint64_t s2 = 0, t2 = 0;
 #pragma unroll
     for (int u = 0; u < kVecs; ++u)
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float d = Vec<T>::get(w[u], i) - ref;
-        const float e = exp2_approx(d * kLog2e);
-        s2[i & 1] += e;
-        t2[i & 1] = fmaf(fmaxf(d, -1e30f), e, t2[i & 1]);  // a term of weight zero adds zero
+      for (int i = 0; i < N / 2; ++i) {
+        const float2 xx = Vec<T>::pair(w[u], i);
+        const uint64_t d2 = add2(pack2(xx.x, xx.y), ref2);
+        const float2 y = unpack2(mul2(d2, scale2)), d = unpack2(d2);
+        const uint64_t e2 = pack2(exp2_approx(y.x), exp2_approx(y.y));
+        s2 = add2(s2, e2);
+        // (a term of weight zero adds zero, also where x - m is infinite)
+        t2 = fma2(pack2(fmaxf(d.x, -1e30f), fmaxf(d.y, -1e30f)), e2, t2);
       }
-    a.s += s2[0] + s2[1];
-    a.t += t2[0] + t2[1];
+    const float2 s1 = unpack2(s2), t1 = unpack2(t2);
+    a.s += s1.x + s1.y;
+    a.t += t1.x + t1.y;
     if (TOP) {
-      if (c == v0) {
-        // threshold: the top-th largest of the threads' maxima, taken out one by one by the first
-        // warp; -inf may stand for no logit at all, so it is no threshold
-        unsigned* best = reinterpret_cast<unsigned*>(list);
-        best[tid] = order_key(bm);
-        __syncthreads();
-        if (tid < 32) {
-          unsigned k[kThreads / 32], kth = 0;
+      Key best = 0;
+      if (chunk == 0) {
+        // the lane's best key (the first of equal logits)
+        int at = 0;
 #pragma unroll
-          for (int i = 0; i < kThreads / 32; ++i) k[i] = best[i * 32 + tid];
-          for (int n = 0; n < top; ++n) {
-            unsigned mine = 0;
+        for (int u = kVecs - 1; u >= 0; --u)
 #pragma unroll
-            for (int i = 0; i < kThreads / 32; ++i) mine = max(mine, k[i]);
-            kth = __reduce_max_sync(0xffffffffu, mine);
-            const unsigned owners = __ballot_sync(0xffffffffu, mine == kth);
-            bool taken = tid != __ffs(owners) - 1;
-#pragma unroll
-            for (int i = 0; i < kThreads / 32; ++i)
-              if (!taken && k[i] == kth) {
-                k[i] = 0;
-                taken = true;
-              }
+          for (int i = N / 2 - 1; i >= 0; --i) {
+            const float2 xx = Vec<T>::pair(w[u], i);
+            if (xx.y == bm) at = u * kThreads * N + 2 * i + 1;
+            if (xx.x == bm) at = u * kThreads * N + 2 * i;
           }
-          if (tid == 0) tau_sh = kth > order_key(-INFINITY) ? (static_cast<unsigned long long>(kth) << 32) - 1 : 0;
-        }
+        if (bm > -INFINITY) best = make_key(bm, (c + tid) * N - head + at);
+        mine = sort_keys(best);
+        gather();
         __syncthreads();
-        tau = tau_sh;
-        tau_x = key_value(static_cast<unsigned>(tau >> 32));
       }
-      // elements above the threshold into the list; those that found no place wait for the cut
-      uint32_t pending = 0;
-      if (!(bm < tau_x)) {
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int v = c + u * kThreads + tid, k = v * N + i - head;
-            if (v < v1 && k >= 0 && k < vocab && make_key(Vec<T>::get(w[u], i), k) > tau) pending |= 1u << (u * N + i);
+      floor = max(floor, *const_cast<volatile Key*>(&tau_sh));
+      const float fx = key_value(static_cast<unsigned>(floor >> 32));
+      unsigned lanes = __ballot_sync(0xffffffffu, !(bm < fx));
+      if (lanes) {
+        // a lane with something above the threshold has its logits looked at by the whole warp, one
+        // a lane, from shared memory (rolled code: unrolled over the registers it costs more in
+        // instruction fetches than it does in work)
+        __syncwarp();  // the other lanes' logits have landed too
+#pragma unroll 1
+        while (lanes) {
+          const int src = __ffs(lanes) - 1;
+          lanes &= lanes - 1;
+          const int v = c + lane / N * kThreads + warp * 32 + src, k = v * N + lane % N - head;
+          Key key = 0;
+          if (lane < kVecs * N && v < v1 && k >= 0 && k < vocab)
+            key = make_key(to_float(reinterpret_cast<const T*>(here + lane / N * kThreads + warp * 32 + src)[lane % N]), k);
+          const Key known = __shfl_sync(0xffffffffu, best, src);
+          unsigned votes = __ballot_sync(0xffffffffu, key > floor && key != known);
+#pragma unroll 1
+          while (votes) {
+            const Key next = __shfl_sync(0xffffffffu, key, __ffs(votes) - 1);
+            votes &= votes - 1;
+            if (next <= floor) continue;  // (the same for the whole warp)
+            const int rank = __popc(__ballot_sync(0xffffffffu, mine > next));
+            const Key up = __shfl_up_sync(0xffffffffu, mine, 1);
+            if (lane == rank) mine = next;
+            if (lane > rank) mine = up;
+            floor = max(floor, __shfl_sync(0xffffffffu, mine, top - 1));
           }
-      }
-      for (;;) {
-        if (pending) {
-#pragma unroll
-          for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-              if (pending >> (u * N + i) & 1u) {
-                const unsigned long long key = make_key(Vec<T>::get(w[u], i), (c + u * kThreads + tid) * N + i - head);
-                const int at = key > tau ? atomicAdd(&count, 1) : 0;
-                if (key > tau && at < kList) list[at] = key;
-                if (key <= tau || at < kList) pending &= ~(1u << (u * N + i));
-              }
         }
-        const bool more = __syncthreads_or(pending != 0);
-        const int n = min(count, kList);
-        if (!more && n <= kCut) break;
-        // cut the list back to its `top` best
-        for_ranks(list, n, [&](int rank, unsigned long long k) {
-          if (rank < top) kept[rank] = k;
-          if (rank == top - 1) tau_sh = k;
-        });
-        __syncthreads();
-        if (tid < top && tid < n) list[tid] = kept[tid];
-        if (tid == 0) count = min(n, top);
-        if (n >= top) {
-          tau = tau_sh;
-          tau_x = key_value(static_cast<unsigned>(tau >> 32));
-        }
-        __syncthreads();
-        if (!more) break;
       }
+      if (chunk > 0 && ((chunk + 1) & chunk) == 0 && chunk + 1 < chunks) gather();
     }
   }
+  if (TOP) gather();
   a = block_join(a);
-  if (TOP) __syncthreads();
-  const int n = TOP ? min(count, kList) : 0;
-  if (ONE) {
-    if (tid == 0) write_row(o, r, a, x, vocab);
-    if (TOP) {
-      const float ls = log_sum(a);
-      for_ranks(list, n, [&](int rank, unsigned long long k) {
-        if (rank < top) {
-          o.top_ids[r * top + rank] = key_index(k);
-          o.top_lp[r * top + rank] = (key_value(static_cast<unsigned>(k >> 32)) - a.m) - ls;
-        }
-      });
-    }
-  } else {
-    if (tid == 0) parts[blockIdx.x] = Part{a, min(n, top)};
-    if (TOP)
-      for_ranks(list, n, [&](int rank, unsigned long long k) {
-        if (rank < top) part_keys[static_cast<int64_t>(blockIdx.x) * top + rank] = k;
-      });
+  if (tid == 0) {
+    if (ONE) write_row(o, r, a, x, vocab);
+    else parts[blockIdx.x] = a;
+  }
+  if (TOP && tid < top) {
+    if (ONE) write_top(o, r, top, a, mine);
+    else part_keys[static_cast<int64_t>(blockIdx.x) * top + tid] = mine;
   }
 }
 
@@ -331,60 +401,62 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const T* __
 template <typename T>
 __global__ void __launch_bounds__(kThreads) token_logprobs_join_kernel(const T* __restrict__ logits, int vocab, int64_t ld,
                                                                       int segments, int top, Outs o,
-                                                                      const Part* __restrict__ parts,
-                                                                      const unsigned long long* __restrict__ part_keys) {
-  __shared__ unsigned long long list[kMaxSegments * kMaxTop];
-  __shared__ int count;
+                                                                      const Sums* __restrict__ parts,
+                                                                      const Key* __restrict__ part_keys) {
+  __shared__ Key lists[kWarps][32];
   pdl_enter();
   const int64_t r = blockIdx.x;
-  const Part* p = parts + r * segments;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Sums a = {-INFINITY, 0.f, 0.f};
-  if (threadIdx.x < segments) a = p[threadIdx.x].a;
-  if (threadIdx.x == 0) count = 0;
-  a = block_join(a);  // (also orders count = 0 before its uses)
-  for (int i = threadIdx.x; i < segments * top; i += kThreads)
-    if (i % top < p[i / top].n) list[atomicAdd(&count, 1)] = part_keys[r * segments * top + i];
-  __syncthreads();
+  if (threadIdx.x < segments) a = parts[r * segments + threadIdx.x];
+  Key mine = 0;
+  if (top > 0) {
+    for (int i = warp; i < segments; i += kWarps)
+      mine = merge_keys(mine, lane < top ? part_keys[(r * segments + i) * top + lane] : 0);
+    lists[warp][lane] = mine;
+  }
+  a = block_join(a);  // (the lists are complete behind its barrier)
   if (threadIdx.x == 0) write_row(o, r, a, logits + r * ld, vocab);
-  const float ls = log_sum(a);
-  for_ranks(list, count, [&](int rank, unsigned long long k) {
-    if (rank < top) {
-      o.top_ids[r * top + rank] = key_index(k);
-      o.top_lp[r * top + rank] = (key_value(static_cast<unsigned>(k >> 32)) - a.m) - ls;
-    }
-  });
+  if (warp == 0 && top > 0) {
+    mine = merge_lists(lists);
+    if (lane < top) write_top(o, r, top, a, mine);
+  }
 }
 
-// Segments a row is split in: enough blocks for four on every SM, each with at least 4096 logits
-// (less work than that is shorter than joining it).
+// Segments a row is split in: enough blocks to fill the GPU once, each with at least 4096 logits
+// (less work than that is shorter than joining it). Splitting further, to even out the last wave,
+// costs more in candidates than it saves: 3000 x 131072 bf16, top 5: 172 us whole, 197 in halves.
 int logprob_segments(int64_t rows, int64_t vocab, int num_sms) {
-  const int64_t want = (4 * static_cast<int64_t>(num_sms) + rows - 1) / rows;
-  if (want <= 2) return 1;  // rows alone fill the GPU
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, vocab / 4096), kMaxSegments)));
+  const int64_t slots = static_cast<int64_t>(num_sms) * (1024 / kThreads);
+  const int64_t want = std::min((slots + rows - 1) / rows, vocab / 4096);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, kMaxSegments)));
 }
 
 template <typename T>
 cudaError_t launch_t(const T* x, int64_t rows, int vocab, int64_t ld, int top, const Outs& o, void* ws, int segments,
                      cudaStream_t stream) {
-  Part* parts = static_cast<Part*>(ws);
-  auto* keys = segments > 1 ? reinterpret_cast<unsigned long long*>(parts + rows * segments) : nullptr;
+  Key* keys = static_cast<Key*>(ws);
+  Sums* parts = segments > 1 ? reinterpret_cast<Sums*>(keys + rows * segments * top) : nullptr;
   const dim3 grid(static_cast<unsigned>(rows * segments));
   auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, dim3(kThreads), 0, stream, x, vocab, ld, segments, top, o, parts, keys);
+    constexpr size_t smem = static_cast<size_t>(kStages) * kChunk * 16;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, grid, dim3(kThreads), smem, stream, x, vocab, ld, segments, top, o, parts, keys);
   };
   if (segments == 1)
     return top > 0 ? go(token_logprobs_kernel<T, true, true>) : go(token_logprobs_kernel<T, false, true>);
   const cudaError_t e = top > 0 ? go(token_logprobs_kernel<T, true, false>) : go(token_logprobs_kernel<T, false, false>);
   if (e != cudaSuccess) return e;
   return launch_pdl(token_logprobs_join_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0, stream, x, vocab,
-                    ld, segments, top, o, static_cast<const Part*>(parts), static_cast<const unsigned long long*>(keys));
+                    ld, segments, top, o, static_cast<const Sums*>(parts), static_cast<const Key*>(keys));
 }
 
 }  // namespace
 
 size_t token_logprobs_ws_bytes(int64_t rows, int64_t vocab, int64_t top, int num_sms) {
   const int segments = logprob_segments(rows, vocab, num_sms);
-  return segments == 1 ? 0 : static_cast<size_t>(rows) * segments * (sizeof(Part) + static_cast<size_t>(top) * 8);
+  return segments == 1 ? 0 : static_cast<size_t>(rows) * segments * (sizeof(Sums) + static_cast<size_t>(top) * 8);
 }
 
 cudaError_t launch_token_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
