@@ -8,13 +8,13 @@
 // The G heads that share a key/value head are rows of one tile (row = token * G + head), so a
 // tile of keys is read once for all of them.
 //
-//   plan_kernel      cuts the step into pieces on the device: per tile of rows the key tiles (64
-//                    positions) it can see, and long tiles into pieces of equal length, so that
-//                    the pieces fill the GPU;
+//   plan_kernel      lays the work of the step (key tiles of every tile of rows and key/value head)
+//                    on one line and cuts it into equal shares, one per resident block; a tile
+//                    that a cut runs through becomes several pieces;
 //   few_rows_kernel  at most 16 rows a sequence (single tokens): memory bound. Four warps take 16
 //                    keys each of every 64-key tile on mma.sync, each with its own running
-//                    softmax, merged at the end;
-//   many_rows_kernel tiles of up to 128 rows on tcgen05;
+//                    softmax, merged at the end of a piece;
+//   many_rows_kernel tiles of up to 256 rows on tcgen05;
 //   merge_kernel     joins the pieces of a split tile.
 // Scores, maxima, sums and accumulators are fp32; the weights are rounded to bf16 for the second
 // product, and the sums add the rounded weights, so that the normalisation matches them.
@@ -31,11 +31,13 @@
 namespace ttq {
 namespace {
 
-constexpr int kKeyTile = 64;       // positions per key tile
 constexpr int kFewRows = 16;       // rows of a tile of few_rows_kernel (one mma.sync block)
-constexpr int kManyRows = 128;     // rows of a tile of many_rows_kernel (one tcgen05 block)
+constexpr int kFewKeys = 64;       // its key tile
+constexpr int kHalfRows = 128;     // rows of one tcgen05 block; many_rows_kernel works on two
+constexpr int kManyKeys = 128;     // its key tile
 constexpr int kPlanThreads = 1024;
-constexpr unsigned kPlanMagic = 0x54545132u;
+constexpr int kPlanTiles = 2048;   // tiles whose data the plan keeps in shared memory
+constexpr unsigned kPlanMagic = 0x54545133u;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ---------------------------------------------------------------- plan
@@ -43,32 +45,34 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct PlanHeader {
   unsigned magic;  // kPlanMagic when the lengths were in range
   int seqs, tokens, max_new, heads, kv_heads, head_dim, window;
-  int pieces;      // pieces of the step (each for every key/value head)
-  int splits;      // tiles of more than one piece
+  int pieces;
+  int splits;      // (tile, key/value head)s of more than one piece
 };
 
-// One piece of a tile's keys. Key tile j of [j0, j1) is tile j of the cache when j < nA, else
-// tile lo + (j - nA): a prefix apart from the window leaves a gap between them.
-struct Piece {
+// One piece of the keys of a tile of rows and a key/value head. Key tile j of [j0, j1) is tile j of
+// the cache when j < nA, else tile lo + (j - nA): a prefix apart from the window leaves a gap.
+struct __align__(16) Piece {
   int seq, tok0, ntok;  // sequence; first token row; tokens of the tile
   int p0;               // position of its first token (negative: before the cache)
   int j0, j1, nA, lo;
   int slot;             // where its partial result goes (-1: it is the whole tile)
   int pre;              // prefix of the sequence
-  int pad0, pad1;
+  int kvh;              // key/value head
+  int pad;
 };
 struct Split {
-  int tok0, ntok, slot0, pieces;
+  int tok0, ntok, slot0, pieces, kvh, pad[3];
 };
 
 // Sizes that follow from the shape alone (same on the host and the device).
 struct PlanLayout {
-  int rows;       // rows of a tile: kFewRows or kManyRows
-  int tq;         // tokens of a tile
-  int row_cap;    // rows a tile can have (partial results are that many rows)
-  int target;     // pieces (over all key/value heads) that fill the GPU
-  int max_tiles, max_slots, max_pieces, max_splits;
-  size_t off_tile_start, off_tiles, off_pieces, off_splits, off_ml, off_acc, bytes;
+  int rows;      // kFewRows or 2 kHalfRows
+  int tq;        // tokens of a tile
+  int row_cap;   // rows a tile can have (partial results are that many rows)
+  int key_tile;  // positions of a key tile
+  int ctas;      // blocks the work is cut for: those resident at once
+  int max_tiles, max_pieces, max_slots, max_splits;
+  size_t off_cta, off_tile_seq, off_tile_at, off_pieces, off_splits, off_ml, off_acc, bytes;
 };
 
 constexpr size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -78,26 +82,29 @@ PlanLayout plan_layout(const PagedShape& s, int num_sms) {
   const int64_t G = s.heads / s.kv_heads;
   // Few rows a sequence go to mma.sync, whose 16-row blocks leave the least work to rows that
   // are not there; more rows to tcgen05.
-  l.rows = s.max_new * G <= kFewRows ? kFewRows : kManyRows;
-  l.tq = static_cast<int>(l.rows / G);
-  l.row_cap = static_cast<int>(std::min<int64_t>(l.tq, s.max_new) * G);
-  l.target = num_sms * (l.rows == kFewRows ? 8 : 2);
+  const bool few = s.max_new * G <= kFewRows;
+  l.rows = few ? kFewRows : 2 * kHalfRows;
+  l.tq = static_cast<int>(few ? kFewRows / G : 2 * (kHalfRows / G));
+  l.row_cap = few ? static_cast<int>(s.max_new * G) : 2 * kHalfRows;
+  l.key_tile = few ? kFewKeys : kManyKeys;
+  l.ctas = num_sms * (few ? 2 : 1);
   l.max_tiles = static_cast<int>(std::min(s.tokens, s.tokens / l.tq + s.seqs));
-  // a tile is split only when it has more than `per` key tiles, per >= (all key tiles x kv heads)
-  // / target, so all split tiles together have at most 2 target / kv_heads pieces
-  l.max_slots = static_cast<int>(2 * l.target / s.kv_heads);
-  l.max_pieces = l.max_tiles + l.max_slots;
-  l.max_splits = std::min(l.max_slots / 2, l.max_tiles);
+  // every cut adds one piece, and at most two of the pieces of a split tile
+  l.max_pieces = static_cast<int>(l.max_tiles * s.kv_heads + l.ctas);
+  l.max_splits = l.ctas;
+  l.max_slots = 2 * l.ctas;
   size_t o = up256(sizeof(PlanHeader));
-  l.off_tile_start = o;
-  o = up256(o + (static_cast<size_t>(s.seqs) + 1) * 4);
-  l.off_tiles = o;
+  l.off_cta = o;
+  o = up256(o + (static_cast<size_t>(l.ctas) + 1) * 4);
+  l.off_tile_seq = o;
+  o = up256(o + static_cast<size_t>(l.max_tiles) * 8);
+  l.off_tile_at = o;
   o = up256(o + static_cast<size_t>(l.max_tiles) * 8);
   l.off_pieces = o;
   o = up256(o + static_cast<size_t>(l.max_pieces) * sizeof(Piece));
   l.off_splits = o;
   o = up256(o + static_cast<size_t>(l.max_splits) * sizeof(Split));
-  const size_t rows = static_cast<size_t>(l.max_slots) * s.kv_heads * l.row_cap;
+  const size_t rows = static_cast<size_t>(l.max_slots) * l.row_cap;
   l.off_ml = o;
   o = up256(o + rows * 8);
   l.off_acc = o;
@@ -110,13 +117,13 @@ struct TileKeys {
   int total, nA, lo;
 };
 // Key tiles that the tokens at positions p0 .. p0 + ntok - 1 can see.
-__device__ __forceinline__ TileKeys tile_keys(int p0, int ntok, int pre, int window) {
-  const int hi_pos = max(p0 + ntok, 0);                                  // past the last position seen
+__device__ __forceinline__ TileKeys tile_keys(int p0, int ntok, int pre, int window, int kt) {
+  const int hi_pos = max(p0 + ntok, 0);  // past the last position seen
   const int lo_pos = window > 0 ? max(0, p0 - window + 1) : 0;
   TileKeys t;
-  t.nA = (pre + kKeyTile - 1) / kKeyTile;
-  t.lo = lo_pos / kKeyTile;
-  int hi = max((hi_pos + kKeyTile - 1) / kKeyTile, t.nA);
+  t.nA = (pre + kt - 1) / kt;
+  t.lo = lo_pos / kt;
+  int hi = max((hi_pos + kt - 1) / kt, t.nA);
   if (t.nA >= t.lo) {  // the prefix reaches the window: one range
     if (t.nA > 0) t.lo = 0;
     t.nA = 0;
@@ -125,6 +132,10 @@ __device__ __forceinline__ TileKeys tile_keys(int p0, int ntok, int pre, int win
   t.total = t.nA + hi - t.lo;
   return t;
 }
+
+// Units of work of a tile with that many key tiles: starting and finishing one costs about as much
+// as two key tiles.
+__device__ __forceinline__ int tile_cost(int total) { return total + 2; }
 
 // Exclusive scan over the block (kPlanThreads threads); *total gets the sum.
 __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* total, uint64_t* sh) {
@@ -160,14 +171,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
                                                            const int* __restrict__ prefix, PlanHeader h, PlanLayout l,
                                                            uint8_t* plan, unsigned* err) {
   __shared__ uint64_t sh[33];
-  __shared__ int piece_at[kPlanThreads + 1];
+  __shared__ int2 tile_seq_sh[kPlanTiles];
+  __shared__ uint64_t tile_at_sh[kPlanTiles];
   pdl_enter();
   const int tid = threadIdx.x;
-  int* tile_start = reinterpret_cast<int*>(plan + l.off_tile_start);
-  int2* tiles = reinterpret_cast<int2*>(plan + l.off_tiles);  // (sequence, key tiles)
+  PlanHeader* out = reinterpret_cast<PlanHeader*>(plan);
+  int* cta_first = reinterpret_cast<int*>(plan + l.off_cta);
   Piece* pieces = reinterpret_cast<Piece*>(plan + l.off_pieces);
   Split* splits = reinterpret_cast<Split*>(plan + l.off_splits);
-  PlanHeader* out = reinterpret_cast<PlanHeader*>(plan);
+  // per tile: (sequence, first token in it), and where its work begins on the line
+  const bool small = l.max_tiles <= kPlanTiles;
+  int2* tile_seq = small ? tile_seq_sh : reinterpret_cast<int2*>(plan + l.off_tile_seq);
+  uint64_t* tile_at = small ? tile_at_sh : reinterpret_cast<uint64_t*>(plan + l.off_tile_at);
   // lengths in range?
   bool bad = false;
   for (int b = tid; b < h.seqs; b += kPlanThreads) {
@@ -183,101 +198,88 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
     }
     return;
   }
-  // first tile of every sequence
+  // tiles of every sequence
   uint64_t sum = 0;
   for (int b0 = 0; b0 < h.seqs; b0 += kPlanThreads) {
     const int b = b0 + tid;
     const int n = b < h.seqs ? q_start[b + 1] - q_start[b] : 0;
     uint64_t tot;
-    const uint64_t at = block_scan((n + l.tq - 1) / l.tq, &tot, sh);
-    if (b < h.seqs) tile_start[b] = static_cast<int>(sum + at);
+    const int at = static_cast<int>(sum + block_scan((n + l.tq - 1) / l.tq, &tot, sh));
+    for (int i = 0; i * l.tq < n; ++i) tile_seq[at + i] = make_int2(b, i * l.tq);
     sum += tot;
   }
   const int ntiles = static_cast<int>(sum);
-  if (tid == 0) tile_start[h.seqs] = ntiles;
   __syncthreads();
-  // key tiles of every tile of rows
-  uint64_t all = 0;
+  auto tile_of = [&](int t, Piece* p) -> TileKeys {
+    const int2 ts = tile_seq[t];
+    const int s0 = q_start[ts.x], n = q_start[ts.x + 1] - s0, L = kv_len[ts.x];
+    p->seq = ts.x;
+    p->tok0 = s0 + ts.y;
+    p->ntok = min(l.tq, n - ts.y);
+    p->p0 = L - n + ts.y;
+    p->pre = prefix ? max(0, min(prefix[ts.x], L)) : 0;
+    const TileKeys k = tile_keys(p->p0, p->ntok, p->pre, h.window, l.key_tile);
+    p->nA = k.nA;
+    p->lo = k.lo;
+    return k;
+  };
+  // where the work of every tile begins (a tile's key/value heads follow each other)
+  uint64_t work = 0;
   for (int t0 = 0; t0 < ntiles; t0 += kPlanThreads) {
     const int t = t0 + tid;
-    int tot_keys = 0;
+    uint64_t cost = 0, tot;
     if (t < ntiles) {
-      int lo = 0, hi = h.seqs;  // tile_start[lo] <= t < tile_start[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (tile_start[mid] <= t) lo = mid; else hi = mid;
-      }
-      const int s0 = q_start[lo], n = q_start[lo + 1] - s0, i0 = (t - tile_start[lo]) * l.tq, L = kv_len[lo];
-      const int pre = prefix ? max(0, min(prefix[lo], L)) : 0;
-      tot_keys = tile_keys(L - n + i0, min(l.tq, n - i0), pre, h.window).total;
-      tiles[t] = make_int2(lo, tot_keys);
+      Piece p;
+      cost = static_cast<uint64_t>(tile_cost(tile_of(t, &p).total)) * h.kv_heads;
     }
-    uint64_t tot;
-    block_scan(tot_keys, &tot, sh);
-    all += tot;
+    const uint64_t at = work + block_scan(cost, &tot, sh);
+    if (t < ntiles) tile_at[t] = at;
+    work += tot;
   }
-  const uint64_t work = all * h.kv_heads;
-  const int per = static_cast<int>(max(static_cast<uint64_t>(1), (work + l.target - 1) / l.target));
-  // pieces: scanned as (pieces, slots, splits) in 26 + 19 + 19 bits
+  __syncthreads();
+  // equal shares; a share shorter than a few key tiles is not worth its start
+  const uint64_t share = max(static_cast<uint64_t>(4), (work + l.ctas - 1) / l.ctas);
+  // pieces of every item (tile, kv head), scanned as (pieces, slots, splits) in 32 + 16 + 16 bits
+  const int items = ntiles * h.kv_heads;
   uint64_t base = 0;
-  for (int t0 = 0; t0 < ntiles; t0 += kPlanThreads) {
-    const int t = t0 + tid;
-    int np = 0, keys = 0, b = 0;
-    if (t < ntiles) {
-      b = tiles[t].x;
-      keys = tiles[t].y;
-      np = max(1, (keys + per - 1) / per);
+  for (int i0 = 0; i0 < items; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    Piece p = {};
+    TileKeys k = {};
+    uint64_t a = 0, v = 0, tot, c0 = 0;
+    int np = 0, cost = 1;
+    if (i < items) {
+      const int t = i / h.kv_heads;
+      p.kvh = i - t * h.kv_heads;
+      k = tile_of(t, &p);
+      cost = tile_cost(k.total);
+      a = tile_at[t] + static_cast<uint64_t>(p.kvh) * cost;
+      c0 = a / share;
+      np = static_cast<int>((a + cost - 1) / share - c0) + 1;
+      v = static_cast<uint64_t>(np) << 32 | (np > 1 ? static_cast<uint64_t>(np) << 16 | 1u : 0u);
     }
-    uint64_t tot;
-    const uint64_t v = static_cast<uint64_t>(np) << 38 | (np > 1 ? static_cast<uint64_t>(np) << 19 | 1u : 0u);
-    const uint64_t at = block_scan(v, &tot, sh);
-    piece_at[tid] = static_cast<int>(at >> 38);
-    if (tid == 0) piece_at[kPlanThreads] = static_cast<int>(tot >> 38);
-    const uint64_t here = base + at;
-    const int slot0 = static_cast<int>(here >> 19 & 0x7ffff), split = static_cast<int>(here & 0x7ffff);
-    if (t < ntiles) {
-      if (np > 1 && split < l.max_splits) {
-        const int s0 = q_start[b], n = q_start[b + 1] - s0, i0 = (t - tile_start[b]) * l.tq;
-        splits[split] = Split{s0 + i0, min(l.tq, n - i0), slot0, np};
-      }
-      tiles[t] = make_int2(b, np > 1 ? slot0 : -1);
-    }
-    __syncthreads();
-    const int first = static_cast<int>(base >> 38);
-    const int count = piece_at[kPlanThreads];
-    for (int p = tid; p < count; p += kPlanThreads) {
-      int lo = 0, hi = kPlanThreads;  // piece_at[lo] <= p < piece_at[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (piece_at[mid] <= p) lo = mid; else hi = mid;
-      }
-      // tiles past the last have no pieces, so the largest index at or below p is the tile's own
-      const int tt = t0 + lo, bb = tiles[tt].x, slot = tiles[tt].y;
-      const int k = p - piece_at[lo], pcs = piece_at[lo + 1] - piece_at[lo];
-      const int s0 = q_start[bb], n = q_start[bb + 1] - s0, i0 = (tt - tile_start[bb]) * l.tq, L = kv_len[bb];
-      Piece pc;
-      pc.seq = bb;
-      pc.tok0 = s0 + i0;
-      pc.ntok = min(l.tq, n - i0);
-      pc.p0 = L - n + i0;
-      pc.pre = prefix ? max(0, min(prefix[bb], L)) : 0;
-      const TileKeys tk = tile_keys(pc.p0, pc.ntok, pc.pre, h.window);
-      pc.nA = tk.nA;
-      pc.lo = tk.lo;
-      pc.j0 = static_cast<int>(static_cast<int64_t>(tk.total) * k / pcs);
-      pc.j1 = static_cast<int>(static_cast<int64_t>(tk.total) * (k + 1) / pcs);
-      pc.slot = slot < 0 ? -1 : slot + k;
-      pc.pad0 = pc.pad1 = 0;
-      if (first + p < l.max_pieces) pieces[first + p] = pc;
-    }
+    const uint64_t here = base + block_scan(v, &tot, sh);
     base += tot;
-    __syncthreads();  // piece_at is rewritten
+    const int first = static_cast<int>(here >> 32), slot0 = static_cast<int>(here >> 16 & 0xffff);
+    const int split = static_cast<int>(here & 0xffff);
+    if (np > 1 && split < l.max_splits) splits[split] = Split{p.tok0, p.ntok, slot0, np, p.kvh, {0, 0, 0}};
+    for (int n = 0; n < np; ++n) {
+      const uint64_t lo = max(a, (c0 + n) * share) - a, hi = min(a + cost, (c0 + n + 1) * share) - a;
+      p.j0 = static_cast<int>(lo * k.total / cost);
+      p.j1 = static_cast<int>(hi * k.total / cost);
+      p.slot = np > 1 ? slot0 + n : -1;
+      if (first + n < l.max_pieces) pieces[first + n] = p;
+      if (a + lo == (c0 + n) * share) cta_first[c0 + n] = first + n;  // (c0 + n < ctas: share covers the work)
+    }
   }
+  const int npieces = static_cast<int>(base >> 32);
+  for (uint64_t c = (work + share - 1) / share + tid; c <= static_cast<uint64_t>(l.ctas); c += kPlanThreads)
+    cta_first[c] = npieces;
   if (tid == 0) {
     h.magic = kPlanMagic;
-    h.pieces = static_cast<int>(base >> 38);
-    h.splits = static_cast<int>(base & 0x7ffff);
-    if (h.pieces > l.max_pieces || h.splits > l.max_splits || static_cast<int>(base >> 19 & 0x7ffff) > l.max_slots) {
+    h.pieces = npieces;
+    h.splits = static_cast<int>(base & 0xffff);
+    if (npieces > l.max_pieces || h.splits > l.max_splits || static_cast<int>(base >> 16 & 0xffff) > l.max_slots) {
       h.magic = 0;  // cannot happen (see plan_layout); never run past the buffers all the same
       h.pieces = h.splits = 0;
       atomicOr(err, kErrLayout);
@@ -291,10 +293,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
 struct PagedArgs {
   PlanHeader want;  // the shape this call was given
   const uint8_t* plan;
-  size_t off_pieces, off_splits;
-  float* acc;       // partial accumulators [slot][kv head][row][D], unnormalised
+  size_t off_cta, off_pieces, off_splits;
+  float* acc;       // partial accumulators [slot][row][D], unnormalised
   float2* ml;       // their (maximum in log2 units, sum)
-  int row_cap, G;
+  int row_cap, G, stages;
   const int* table;
   int width, num_pages, page_size, page_log2;
   float scale_log2;  // log2(e) / sqrt(D)
@@ -350,17 +352,32 @@ __device__ __forceinline__ Needed needed_keys(const Piece& p, int window) {
 
 __device__ __forceinline__ int key_tile(const Piece& p, int j) { return j < p.nA ? j : p.lo + (j - p.nA); }
 
+// Pieces [first, end) of block `cta`.
+__device__ __forceinline__ int2 cta_pieces(const PagedArgs& a, int cta) {
+  const int* f = reinterpret_cast<const int*>(a.plan + a.off_cta) + cta;
+  return make_int2(f[0], f[1]);
+}
+__device__ __forceinline__ Piece load_piece(const PagedArgs& a, int i) {
+  Piece p;
+  const uint4* src = reinterpret_cast<const uint4*>(a.plan + a.off_pieces) + 3 * static_cast<int64_t>(i);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) reinterpret_cast<uint4*>(&p)[k] = src[k];
+  return p;
+}
+
 // Page table entries of the key tiles of a piece, read ahead by a whole warp: lane i holds page
 // i % ppt of tile i / ppt of a group of 32 / ppt tiles (ppt pages a tile).
+template <int KT>
 struct PageFeed {
+  static constexpr int kLog2 = KT == 128 ? 7 : 6;
   int ppt_log2, cur, next, group;
   const int* row;
   __device__ __forceinline__ int fetch(const PagedArgs& a, const Piece& p, int jg, const Needed& nd) {
     const int lane = threadIdx.x & 31;
     const int j = jg + (lane >> ppt_log2);
     if (j >= p.j1) return -1;
-    const int pos = key_tile(p, j) * kKeyTile + ((lane & ((1 << ppt_log2) - 1)) << a.page_log2);
-    const int end = ppt_log2 > 0 ? pos + a.page_size : pos + kKeyTile;
+    const int pos = key_tile(p, j) * KT + ((lane & ((1 << ppt_log2) - 1)) << a.page_log2);
+    const int end = ppt_log2 > 0 ? pos + a.page_size : pos + KT;
     if (!nd.any(pos, end)) return -1;  // no token sees it: reads as zeros
     const int pi = pos >> a.page_log2;
     const int page = pi < a.width ? row[pi] : -1;
@@ -371,7 +388,7 @@ struct PageFeed {
     return page;
   }
   __device__ __forceinline__ void start(const PagedArgs& a, const Piece& p, const Needed& nd) {
-    ppt_log2 = a.page_log2 < 6 ? 6 - a.page_log2 : 0;
+    ppt_log2 = a.page_log2 < kLog2 ? kLog2 - a.page_log2 : 0;
     row = a.table + static_cast<int64_t>(p.seq) * a.width;
     group = p.j0;
     cur = fetch(a, p, group, nd);
@@ -387,7 +404,7 @@ struct PageFeed {
       next = fetch(a, p, group + per, nd);
     }
     const int lane = threadIdx.x & 31;
-    const int inside = ppt_log2 == 0 ? (key_tile(p, j) * kKeyTile) & (a.page_size - 1) : 0;
+    const int inside = ppt_log2 == 0 ? (key_tile(p, j) * KT) & (a.page_size - 1) : 0;
     *z = cur < 0 ? a.num_pages << a.page_log2 : (cur << a.page_log2) + inside;
     return (lane >> ppt_log2) == j - group;
   }
@@ -395,18 +412,22 @@ struct PageFeed {
 
 // ---------------------------------------------------------------- few rows: mma.sync
 
-constexpr int kFewThreads = 160;  // 4 warps of products, 1 of copies
+constexpr int kFewThreads = 160;   // 4 warps of products, 1 of copies
+constexpr int kFewMaxStages = 8;
 
+// smem: a ring of stages (K and V of one key tile, in boxes of 64 channels), then the exchange of
+// the warps' results [4][row_cap][D]. Two CTAs share an SM; each takes as many stages as fit.
 template <int D>
 struct FewLayout {
-  static constexpr int kStages = D == 128 ? 3 : 4;
-  static constexpr uint32_t kBox = kKeyTile * 128;
-  static constexpr uint32_t kTile = (D / 64) * kBox;        // K or V of one tile
+  static constexpr uint32_t kBox = kFewKeys * 128;
+  static constexpr uint32_t kTile = (D / 64) * kBox;
   static constexpr uint32_t kStage = 2 * kTile;
-  static constexpr uint32_t kRing = kStages * kStage;       // reused by the final merge
-  static constexpr size_t kSmem = kRing + 1024;
+  static constexpr uint32_t kBudget = 111 * 1024;  // of the 113 KB a CTA may take, less the static part
+  static int stages(int row_cap) {
+    return std::min<int>(kFewMaxStages, (kBudget - 1024 - 4 * row_cap * D * 4) / kStage);
+  }
+  static size_t smem(int row_cap) { return 1024 + static_cast<size_t>(stages(row_cap)) * kStage + 4 * row_cap * D * 4; }
 };
-static_assert(FewLayout<128>::kRing >= 4 * kFewRows * 128 * 4 && FewLayout<64>::kRing >= 4 * kFewRows * 64 * 4, "");
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -428,18 +449,32 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The warps that multiply meet without the one that copies; true when `v` is true of any of them.
+__device__ __forceinline__ bool few_any(bool v) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(v ? 1 : 0)
+      : "memory");
+  return r != 0;
+}
+
 template <int D>
-__global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
-                                                               const __grid_constant__ CUtensorMap tm_v,
-                                                               const PagedArgs a) {
+__global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
+                                                                  const __grid_constant__ CUtensorMap tm_v,
+                                                                  const PagedArgs a) {
   using Lay = FewLayout<D>;
-  constexpr int S = Lay::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bar_full[S], bar_empty[S];
+  __shared__ uint64_t bar_full[kFewMaxStages], bar_empty[kFewMaxStages];
   __shared__ int abort_sh;
   __shared__ float m_sh[4][kFewRows], l_sh[4][kFewRows];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
+  const int S = a.stages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t b_full = smem_addr(bar_full), b_empty = smem_addr(bar_empty);
   volatile int* abort_flag = &abort_sh;
@@ -460,299 +495,339 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const __grid_cons
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err.word, kErrRange);
     return;
   }
-  const int kvh = static_cast<int>(blockIdx.x) % hdr.kv_heads;
-  const int pi = static_cast<int>(blockIdx.x) / hdr.kv_heads;
-  if (pi >= hdr.pieces) return;
-  const Piece p = reinterpret_cast<const Piece*>(a.plan + a.off_pieces)[pi];
-  const Needed nd = needed_keys(p, hdr.window);
-  const int nj = p.j1 - p.j0;
-  const int G = a.G, rows = p.ntok * G;
-
-  float o[D / 8][4];
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-  float m[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};
+  const int2 range = cta_pieces(a, blockIdx.x);
+  if (range.x >= range.y) return;
+  const int G = a.G;
+  int st = 0, ph = 0;  // stage of the ring and its turn
 
   if (warp == 4) {
     // ------------------------------------------------------------ copies
-    PageFeed feed;
-    feed.start(a, p, nd);
-    int jj = 0;
-    for (; jj < nj; ++jj) {
-      const int st = jj % S;
-      bool ok = true;
-      if (jj >= S) ok = mbar_wait(b_empty + 8 * st, (jj / S - 1) & 1, a.err, abort_flag);
-      if (!warp_all(ok)) break;
-      if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * st, Lay::kStage);
-      __syncwarp();
-      int z;
-      if (feed.mine(a, p, p.j0 + jj, nd, &z)) {
-        const uint32_t ks = base + st * Lay::kStage + (lane & ((1 << feed.ppt_log2) - 1)) * (a.page_size * 128);
+    int issued = 0;
+    Piece next = load_piece(a, range.x);
+    bool ok = true;
+    for (int pi = range.x; ok && pi < range.y; ++pi) {
+      const Piece p = next;
+      if (pi + 1 < range.y) next = load_piece(a, pi + 1);
+      const Needed nd = needed_keys(p, hdr.window);
+      PageFeed<kFewKeys> feed;
+      feed.start(a, p, nd);
+      for (int j = p.j0; j < p.j1; ++j) {
+        if (issued >= S && !warp_all(mbar_wait(b_empty + 8 * st, ph ^ 1, a.err, abort_flag))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * st, Lay::kStage);
+        __syncwarp();
+        int z;
+        if (feed.mine(a, p, j, nd, &z)) {
+          const uint32_t ks = base + st * Lay::kStage + (lane & ((1 << feed.ppt_log2) - 1)) * (a.page_size * 128);
 #pragma unroll
-        for (int bx = 0; bx < D / 64; ++bx) tma_load_3d(ks + bx * Lay::kBox, &tm_k, b_full + 8 * st, 64 * bx, kvh, z);
+          for (int bx = 0; bx < D / 64; ++bx) tma_load_3d(ks + bx * Lay::kBox, &tm_k, b_full + 8 * st, 64 * bx, p.kvh, z);
 #pragma unroll
-        for (int bx = 0; bx < D / 64; ++bx)
-          tma_load_3d(ks + Lay::kTile + bx * Lay::kBox, &tm_v, b_full + 8 * st, 64 * bx, kvh, z);
+          for (int bx = 0; bx < D / 64; ++bx)
+            tma_load_3d(ks + Lay::kTile + bx * Lay::kBox, &tm_v, b_full + 8 * st, 64 * bx, p.kvh, z);
+        }
+        __syncwarp();
+        ++issued;
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
+        }
       }
-      __syncwarp();
     }
     if (lane == 0 && *abort_flag) {
-      for (int k = max(0, jj - S); k < jj; ++k) attn_drain(b_full + 8 * (k % S), (k / S) & 1, a.err);
+      // every copy this CTA started lands before its shared memory is released: the last use of
+      // every stage
+      for (int k = 0; k < min(issued, S); ++k) {
+        if (--st < 0) {
+          st = S - 1;
+          ph ^= 1;
+        }
+        attn_drain(b_full + 8 * st, ph, a.err);
+      }
     }
   } else {
     // ------------------------------------------------------------ products: 16 keys of every tile
     const int r0 = lane >> 2, c0 = (lane & 3) * 2;
-    uint32_t qa[D / 16][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = r0 + 8 * i;
-      const __nv_bfloat16* qr = a.q + (p.tok0 + r / G) * a.ld_q + (kvh * G + r % G) * D;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
-          qa[ks][i + 2 * hh] = r < rows ? *reinterpret_cast<const uint32_t*>(qr + ks * 16 + hh * 8 + c0) : 0u;
-    }
     const ScoreMap map = score_map(a);
     const bool biased = a.slopes != nullptr;
-    float slope[2] = {0.f, 0.f};
-    int pos[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = r0 + 8 * i;
-      pos[i] = r < rows ? p.p0 + r / G : -1;
-      if (biased && r < rows) slope[i] = a.slopes[kvh * G + r % G] * kLog2e;
-    }
     const int window = hdr.window > 0 ? hdr.window : 0x7fffffff;
-    // every token of the tile sees all of [sure_lo, p0]
-    const int sure_lo = hdr.window > 0 ? p.p0 + p.ntok - hdr.window : 0;
-    for (int jj = 0; jj < nj; ++jj) {
-      const int st = jj % S;
-      if (!warp_all(mbar_wait(b_full + 8 * st, (jj / S) & 1, a.err, abort_flag))) break;
-      const uint32_t ks = base + st * Lay::kStage, vs = ks + Lay::kTile;
-      const int k0 = key_tile(p, p.j0 + jj) * kKeyTile + warp * 16;  // this warp's first key
-      if (!nd.all(k0, k0 + 16)) {
-        // rows of V that no token sees may hold anything: their weight is zero, so make them zero
-        const int row = warp * 16 + (lane & 15);
-        if (!nd.at(k0 + (lane & 15))) {
-#pragma unroll
-          for (int bx = 0; bx < D / 64; ++bx)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vs + bx * Lay::kBox + row * 128 +
-                                                                             (lane >> 4) * 64 + c * 16),
-                           "r"(0)
-                           : "memory");
-        }
-        fence_proxy_async_smem();  // before a later copy into the same place
-        __syncwarp();
-      }
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      {
-        // lanes 0-7, 8-15: keys 0-7 of 16-byte chunks c, c + 1; lanes 16-31: keys 8-15
-        const int row = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
-        const uint32_t rb = ks + row * 128;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const int ch = 2 * kk + ((lane >> 3) & 1);
-          uint32_t b[4];
-          ldsm_x4(rb + (ch >> 3) * Lay::kBox + (((ch & 7) ^ (row & 7)) << 4), b);
-          mma_16816(s[0], qa[kk], b[0], b[1]);
-          mma_16816(s[1], qa[kk], b[2], b[3]);
-        }
-      }
-      float mx[2] = {m[0], m[1]};
-      const bool sure = k0 >= sure_lo && k0 + 15 <= p.p0;
-#pragma unroll
-      for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = e >> 1, k = k0 + nb * 8 + c0 + (e & 1);
-          float v = map(s[nb][e]);
-          if (biased) v = fmaf(slope[i], static_cast<float>(k - pos[i]), v);
-          if (!sure) {
-            const bool seen = k < p.pre || (k <= pos[i] && pos[i] - k < window);
-            v = seen ? v : -FLT_MAX;
-          }
-          s[nb][e] = v;
-          mx[i] = fmaxf(mx[i], v);
-        }
+    float* ex = reinterpret_cast<float*>(smem_raw + (base - raw) + S * Lay::kStage);
+    Piece next = load_piece(a, range.x);
+    bool ok = true;
+    for (int pi = range.x; pi < range.y; ++pi) {
+      const Piece p = next;
+      if (pi + 1 < range.y) next = load_piece(a, pi + 1);
+      const Needed nd = needed_keys(p, hdr.window);
+      const int rows = p.ntok * G;
+      uint32_t qa[D / 16][4];
+      float slope[2] = {0.f, 0.f};
+      int pos[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-      }
-      if (__any_sync(0xffffffffu, mx[0] != m[0] || mx[1] != m[1])) {
-        const float f0 = exp2_approx(m[0] - mx[0]), f1 = exp2_approx(m[1] - mx[1]);
+        const int r = r0 + 8 * i;
+        const __nv_bfloat16* qr = a.q + (p.tok0 + r / G) * a.ld_q + (p.kvh * G + r % G) * D;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= f0;
-          o[i][1] *= f0;
-          o[i][2] *= f1;
-          o[i][3] *= f1;
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh)
+            qa[ks][i + 2 * hh] = r < rows ? *reinterpret_cast<const uint32_t*>(qr + ks * 16 + hh * 8 + c0) : 0u;
+        pos[i] = r < rows ? p.p0 + r / G : -1;
+        if (biased && r < rows) slope[i] = a.slopes[p.kvh * G + r % G] * kLog2e;
+      }
+      float o[D / 8][4];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+      float m[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};
+      // every token of the tile sees all of [sure_lo, p0]
+      const int sure_lo = hdr.window > 0 ? p.p0 + p.ntok - hdr.window : 0;
+      for (int j = p.j0; j < p.j1; ++j) {
+        if (!warp_all(mbar_wait(b_full + 8 * st, ph, a.err, abort_flag))) {
+          ok = false;
+          break;
         }
-        l[0] *= f0;
-        l[1] *= f1;
-        m[0] = mx[0];
-        m[1] = mx[1];
-      }
-      // no visible key yet: a reference of zero keeps the weights of hidden keys at zero
-      const float ref0 = m[0] == -FLT_MAX ? 0.f : m[0], ref1 = m[1] == -FLT_MAX ? 0.f : m[1];
-      uint32_t pa[4];
+        const uint32_t ks = base + st * Lay::kStage, vs = ks + Lay::kTile;
+        const int k0 = key_tile(p, j) * kFewKeys + warp * 16;  // this warp's first key
+        if (!nd.all(k0, k0 + 16)) {
+          // rows of V that no token sees may hold anything: their weight is zero, so make them zero
+          const int row = warp * 16 + (lane & 15);
+          if (!nd.at(k0 + (lane & 15))) {
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        pa[2 * nb] = pack_bf16x2(exp2_approx(s[nb][0] - ref0), exp2_approx(s[nb][1] - ref0));
-        pa[2 * nb + 1] = pack_bf16x2(exp2_approx(s[nb][2] - ref1), exp2_approx(s[nb][3] - ref1));
-        l[0] += bf16lo_to_f32(pa[2 * nb]) + bf16hi_to_f32(pa[2 * nb]);
-        l[1] += bf16lo_to_f32(pa[2 * nb + 1]) + bf16hi_to_f32(pa[2 * nb + 1]);
-      }
-      {
-        // lanes 0-15: keys 0-15 of chunk c; lanes 16-31: of chunk c + 1
-        const int row = warp * 16 + (lane & 15);
-        const uint32_t rb = vs + row * 128;
+            for (int bx = 0; bx < D / 64; ++bx)
 #pragma unroll
-        for (int cc = 0; cc < D / 16; ++cc) {
-          const int ch = 2 * cc + (lane >> 4);
-          uint32_t b[4];
-          ldsm_x4_trans(rb + (ch >> 3) * Lay::kBox + (((ch & 7) ^ (row & 7)) << 4), b);
-          mma_16816(o[2 * cc], pa, b[0], b[1]);
-          mma_16816(o[2 * cc + 1], pa, b[2], b[3]);
+              for (int c = 0; c < 4; ++c)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vs + bx * Lay::kBox + row * 128 +
+                                                                               (lane >> 4) * 64 + c * 16),
+                             "r"(0)
+                             : "memory");
+          }
+          fence_proxy_async_smem();  // before a later copy into the same place
+          __syncwarp();
+        }
+        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        {
+          // lanes 0-7, 8-15: keys 0-7 of 16-byte chunks c, c + 1; lanes 16-31: keys 8-15
+          const int row = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+          const uint32_t rb = ks + row * 128;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const int ch = 2 * kk + ((lane >> 3) & 1);
+            uint32_t b[4];
+            ldsm_x4(rb + (ch >> 3) * Lay::kBox + (((ch & 7) ^ (row & 7)) << 4), b);
+            mma_16816(s[0], qa[kk], b[0], b[1]);
+            mma_16816(s[1], qa[kk], b[2], b[3]);
+          }
+        }
+        float mx[2] = {m[0], m[1]};
+        const bool sure = k0 >= sure_lo && k0 + 15 <= p.p0;
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = e >> 1, k = k0 + nb * 8 + c0 + (e & 1);
+            float v = map(s[nb][e]);
+            if (biased) v = fmaf(slope[i], static_cast<float>(k - pos[i]), v);
+            if (!sure) {
+              const bool seen = k < p.pre || (k <= pos[i] && pos[i] - k < window);
+              v = seen ? v : -FLT_MAX;
+            }
+            s[nb][e] = v;
+            mx[i] = fmaxf(mx[i], v);
+          }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+        }
+        if (__any_sync(0xffffffffu, mx[0] != m[0] || mx[1] != m[1])) {
+          const float f0 = exp2_approx(m[0] - mx[0]), f1 = exp2_approx(m[1] - mx[1]);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[i][0] *= f0;
+            o[i][1] *= f0;
+            o[i][2] *= f1;
+            o[i][3] *= f1;
+          }
+          l[0] *= f0;
+          l[1] *= f1;
+          m[0] = mx[0];
+          m[1] = mx[1];
+        }
+        // no visible key yet: a reference of zero keeps the weights of hidden keys at zero
+        const float ref0 = m[0] == -FLT_MAX ? 0.f : m[0], ref1 = m[1] == -FLT_MAX ? 0.f : m[1];
+        uint32_t pa[4];
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+          pa[2 * nb] = pack_bf16x2(exp2_approx(s[nb][0] - ref0), exp2_approx(s[nb][1] - ref0));
+          pa[2 * nb + 1] = pack_bf16x2(exp2_approx(s[nb][2] - ref1), exp2_approx(s[nb][3] - ref1));
+          l[0] += bf16lo_to_f32(pa[2 * nb]) + bf16hi_to_f32(pa[2 * nb]);
+          l[1] += bf16lo_to_f32(pa[2 * nb + 1]) + bf16hi_to_f32(pa[2 * nb + 1]);
+        }
+        {
+          // lanes 0-15: keys 0-15 of chunk c; lanes 16-31: of chunk c + 1
+          const int row = warp * 16 + (lane & 15);
+          const uint32_t rb = vs + row * 128;
+#pragma unroll
+          for (int cc = 0; cc < D / 16; ++cc) {
+            const int ch = 2 * cc + (lane >> 4);
+            uint32_t b[4];
+            ldsm_x4_trans(rb + (ch >> 3) * Lay::kBox + (((ch & 7) ^ (row & 7)) << 4), b);
+            mma_16816(o[2 * cc], pa, b[0], b[1]);
+            mma_16816(o[2 * cc + 1], pa, b[2], b[3]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_empty + 8 * st);
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_empty + 8 * st);
-    }
+      // the four warps' results joined through the exchange
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if ((lane & 3) == 0) {
-        m_sh[warp][r0 + 8 * i] = m[i];
-        l_sh[warp][r0 + 8 * i] = l[i];
+      for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        if ((lane & 3) == 0) {
+          m_sh[warp][r0 + 8 * i] = m[i];
+          l_sh[warp][r0 + 8 * i] = l[i];
+        }
+        if (r0 + 8 * i < rows) {
+          float* to = ex + (warp * a.row_cap + r0 + 8 * i) * D + c0;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) *reinterpret_cast<float2*>(to + c * 8) = make_float2(o[c][2 * i], o[c][2 * i + 1]);
+        }
       }
+      if (few_any(!ok)) break;  // a wait ran out in some warp: no result, and all four leave together
+      for (int i = threadIdx.x; i < rows * (D / 4); i += 128) {
+        const int r = i / (D / 4), c = i % (D / 4) * 4;
+        float M = -FLT_MAX, Ls = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) M = fmaxf(M, m_sh[w][r]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float f = exp2_approx(m_sh[w][r] - M);
+          const float4 v = *reinterpret_cast<const float4*>(ex + (w * a.row_cap + r) * D + c);
+          Ls = fmaf(l_sh[w][r], f, Ls);
+          acc.x = fmaf(v.x, f, acc.x);
+          acc.y = fmaf(v.y, f, acc.y);
+          acc.z = fmaf(v.z, f, acc.z);
+          acc.w = fmaf(v.w, f, acc.w);
+        }
+        if (p.slot < 0) {
+          const float inv = Ls > 0.f ? __fdiv_rn(1.f, Ls) : 0.f;
+          __nv_bfloat16* dst = a.out + static_cast<int64_t>(p.tok0 + r / G) * a.ld_out + (p.kvh * G + r % G) * D + c;
+          *reinterpret_cast<uint2*>(dst) =
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        } else {
+          const int64_t row = static_cast<int64_t>(p.slot) * a.row_cap + r;
+          *reinterpret_cast<float4*>(a.acc + row * D + c) = acc;
+          if (c == 0) a.ml[row] = make_float2(M, Ls);
+        }
+      }
+      few_any(false);  // the exchange is rewritten by the next piece
     }
   }
-  // a wait that ran out: every copy has landed or been drained, no result
-  __syncthreads();
-  if (abort_sh) return;
-  float* sm = reinterpret_cast<float*>(smem_raw + (base - raw));  // [warp][row][D], the ring is free
-  if (warp < 4) {
-    const int r0 = lane >> 2, c0 = (lane & 3) * 2;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      *reinterpret_cast<float2*>(sm + (warp * kFewRows + r0) * D + i * 8 + c0) = make_float2(o[i][0], o[i][1]);
-      *reinterpret_cast<float2*>(sm + (warp * kFewRows + r0 + 8) * D + i * 8 + c0) = make_float2(o[i][2], o[i][3]);
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < rows * (D / 4); i += kFewThreads) {
-    const int r = i / (D / 4), c = i % (D / 4) * 4;
-    float M = -FLT_MAX, Ls = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, m_sh[w][r]);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float f = exp2_approx(m_sh[w][r] - M);
-      const float4 v = *reinterpret_cast<const float4*>(sm + (w * kFewRows + r) * D + c);
-      Ls = fmaf(l_sh[w][r], f, Ls);
-      acc.x = fmaf(v.x, f, acc.x);
-      acc.y = fmaf(v.y, f, acc.y);
-      acc.z = fmaf(v.z, f, acc.z);
-      acc.w = fmaf(v.w, f, acc.w);
-    }
-    if (p.slot < 0) {
-      const float inv = Ls > 0.f ? __fdiv_rn(1.f, Ls) : 0.f;
-      __nv_bfloat16* dst = a.out + static_cast<int64_t>(p.tok0 + r / G) * a.ld_out + (kvh * G + r % G) * D + c;
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    } else {
-      const int64_t row = (static_cast<int64_t>(p.slot) * hdr.kv_heads + kvh) * a.row_cap + r;
-      *reinterpret_cast<float4*>(a.acc + row * D + c) = acc;
-      if (c == 0) a.ml[row] = make_float2(M, Ls);
-    }
-  }
+  __syncthreads();  // every copy has landed or been drained
 }
 
 // ---------------------------------------------------------------- many rows: tcgen05
 
-constexpr int kManyThreads = 192;       // 6 warps: copies, products, 4 of softmax
-constexpr float kRescaleSlack = 8.0f;   // log2 units a row maximum may rise before O is rescaled
-constexpr uint32_t kRowBox = kManyRows * 128;  // 128 rows x 128 B: a box of Q or P
+// 12 warps: 0-3 and 4-7 the softmax of the two halves (128 rows each, a row a thread), 8 copies,
+// 9 products (10 and 11 only complete the warpgroup, whose registers go to the softmax).
+constexpr int kManyThreads = 384;
+constexpr float kRescaleSlack = 8.0f;          // log2 units a row maximum may rise before O is rescaled
+constexpr uint32_t kRowBox = kHalfRows * 128;  // 128 rows x 128 B: a box of Q, K or V
 
 struct ManyBars {
-  uint64_t q_full;
-  uint64_t k_full[2];
-  uint64_t v_full[2];
-  uint64_t kv_empty[2];
-  uint64_t s_full[2];
-  uint64_t s_free[2];
-  uint64_t p_full;
-  uint64_t o_done;
+  uint64_t full[8], empty[8];  // the ring of K and V tiles
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2];          // S of a half is in tensor memory
+  uint64_t p_full[2];          // its weights are, in the place of S
+  uint64_t o_full[2];          // O of a half holds the piece's result
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
 };
 
-// smem: Q | K0 | K1 | V0 | V1 | P (1024-byte aligned boxes of 64 channels or positions), barriers.
-// Tensor memory: S0, S1 (64 columns each), O (D columns).
+// smem: Q of both halves | ring of tiles K_0 V_0 K_1 V_1 ... (128 positions each), in 1024-byte
+// aligned boxes of 64 channels; barriers. Tensor memory: S of both halves (128 columns each; the
+// weights, two to a column, take the first 64), O of both halves (D columns each).
 template <int D>
 struct ManyLayout {
-  static constexpr uint32_t kBox = kKeyTile * 128;
-  static constexpr uint32_t kQBytes = (D / 64) * kRowBox;
-  static constexpr uint32_t kKVBytes = (D / 64) * kBox;
-  static constexpr uint32_t kOffK = kQBytes;
-  static constexpr uint32_t kOffV = kOffK + 2 * kKVBytes;
-  static constexpr uint32_t kOffP = kOffV + 2 * kKVBytes;
-  static constexpr uint32_t kOffBars = kOffP + kRowBox;
-  static constexpr size_t kSmem = kOffBars + sizeof(ManyBars) + 896;  // the base is 128-byte aligned
-  static constexpr uint32_t kColS0 = 0, kColS1 = kKeyTile, kColO = 2 * kKeyTile;
-  static constexpr uint32_t kTmemCols = 256;
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr uint32_t kTile = (D / 64) * kRowBox;  // Q of a half, or K or V of a key tile
+  static constexpr uint32_t kOffRing = 2 * kTile;
+  static constexpr uint32_t kOffBars = kOffRing + kStages * kTile;
+  static constexpr size_t kSmem = kOffBars + sizeof(ManyBars) + 1024;
+  static constexpr uint32_t kColS = 0, kColO = 2 * kManyKeys;
 };
-static_assert(2 * (ManyLayout<128>::kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+static_assert(ManyLayout<128>::kSmem <= 227 * 1024 && ManyLayout<64>::kSmem <= 227 * 1024, "one CTA per SM");
+static_assert(kManyKeys == kHalfRows, "boxes of Q, K and V are alike");
+
+// D[tmem] (+)= A[tmem] * B[smem]: A bf16, a row a lane, two elements a column.
+__device__ __forceinline__ void umma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// A place in a ring of n, and its turn.
+struct Turn {
+  int at = 0, ph = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++at == n) {
+      at = 0;
+      ph ^= 1;
+    }
+  }
+};
 
 template <int D>
-__global__ void __launch_bounds__(kManyThreads, 2)
+__global__ void __launch_bounds__(kManyThreads, 1)
     many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const PagedArgs a) {
   using Lay = ManyLayout<D>;
+  constexpr int S = Lay::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  if ((base - raw) + Lay::kOffBars + sizeof(ManyBars) > Lay::kSmem) {
-    if (threadIdx.x == 0) atomicOr(a.err.word, kErrLayout);
-    return;
-  }
   ManyBars* bars = reinterpret_cast<ManyBars*>(smem_raw + (base - raw) + Lay::kOffBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &bars->abort_flag;
   const DevErr err = a.err;
-  const uint32_t b_q = smem_addr(&bars->q_full), b_kf = smem_addr(&bars->k_full[0]);
-  const uint32_t b_vf = smem_addr(&bars->v_full[0]), b_ke = smem_addr(&bars->kv_empty[0]);
-  const uint32_t b_sf = smem_addr(&bars->s_full[0]), b_sfree = smem_addr(&bars->s_free[0]);
-  const uint32_t b_p = smem_addr(&bars->p_full), b_o = smem_addr(&bars->o_done), b_drain = smem_addr(&bars->drain);
+  const uint32_t b_full = smem_addr(&bars->full[0]), b_empty = smem_addr(&bars->empty[0]);
+  const uint32_t b_q = smem_addr(&bars->q_full), b_qe = smem_addr(&bars->q_empty);
+  const uint32_t b_s = smem_addr(&bars->s_full[0]), b_p = smem_addr(&bars->p_full[0]);
+  const uint32_t b_o = smem_addr(&bars->o_full[0]);
+  const uint32_t b_drain = smem_addr(&bars->drain);
   pdl_enter();  // the plan, q, k and v are written by kernels ahead in the stream
   const PlanHeader hdr = *reinterpret_cast<const PlanHeader*>(a.plan);
   if (!plan_ok(hdr, a.want)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(err.word, kErrRange);
     return;
   }
-  const int kvh = static_cast<int>(blockIdx.x) % hdr.kv_heads;
-  const int pi = static_cast<int>(blockIdx.x) / hdr.kv_heads;
-  if (pi >= hdr.pieces) return;
+  const int2 range = cta_pieces(a, blockIdx.x);
+  if (range.x >= range.y) return;
   if (threadIdx.x == 0) {
-    mbar_init(b_q, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(b_kf + 8 * i, 1);
-      mbar_init(b_vf + 8 * i, 1);
-      mbar_init(b_ke + 8 * i, 1);
-      mbar_init(b_sf + 8 * i, 1);
-      mbar_init(b_sfree + 8 * i, 4);  // one arrival per softmax warp
+    for (int i = 0; i < S; ++i) {
+      mbar_init(b_full + 8 * i, 1);
+      mbar_init(b_empty + 8 * i, 1);
     }
-    mbar_init(b_p, 4);
-    mbar_init(b_o, 1);
+    mbar_init(b_q, 1);
+    mbar_init(b_qe, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b_s + 8 * i, 1);
+      mbar_init(b_p + 8 * i, 4);  // one arrival per softmax warp
+      mbar_init(b_o + 8 * i, 1);
+    }
     mbar_init(b_drain, 1);
     bars->abort_flag = 0;
     fence_mbar_init();
@@ -760,240 +835,289 @@ __global__ void __launch_bounds__(kManyThreads, 2)
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
-  if (warp == 1) {
-    tmem_alloc(smem_addr(&bars->tmem_base), Lay::kTmemCols);
+  if (warp == 9) {
+    tmem_alloc(smem_addr(&bars->tmem_base), 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  const Piece p = reinterpret_cast<const Piece*>(a.plan + a.off_pieces)[pi];
-  const Needed nd = needed_keys(p, hdr.window);
-  const int nj = p.j1 - p.j0;
-  const int G = a.G, rows = p.ntok * G;
+  const int G = a.G;
+  const int tqh = kHalfRows / G;  // tokens of a half
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ copies
-    PageFeed feed;
-    feed.start(a, p, nd);
-    if (nj > 0 && lane == 0) {
-      // rows are (token, head of the group): a box of G heads x tokens; the rows left over in the
-      // tile are never stored
-      mbar_arrive_expect_tx(b_q, (D / 64) * G * (kManyRows / G) * 128);
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 8) {
+      // ------------------------------------------------------------ copies
+      Turn t;
+      int issued = 0, q_loads = 0;
+      bool ok = true;
+      for (int pi = range.x; ok && pi < range.y; ++pi) {
+        const Piece p = load_piece(a, pi);
+        if (p.j0 >= p.j1) continue;
+        const Needed nd = needed_keys(p, hdr.window);
+        PageFeed<kManyKeys> feed;
+        feed.start(a, p, nd);
+        // Q: rows are (token, head of the group), a box of G heads x tokens a half; the rows left
+        // over in a half are never stored
+        if (q_loads > 0 && !warp_all(mbar_wait(b_qe, (q_loads - 1) & 1, err, abort_flag))) break;
+        if (lane == 0) {
+          const int halves = p.ntok > tqh ? 2 : 1;
+          mbar_arrive_expect_tx(b_q, halves * (D / 64) * G * tqh * 128);
+          for (int h = 0; h < halves; ++h)
 #pragma unroll
-      for (int bx = 0; bx < D / 64; ++bx) tma_load_3d(base + bx * kRowBox, &tm_q, b_q, 64 * bx, kvh * G, p.tok0);
-    }
-    __syncwarp();
-    int j = 0;
-    for (; j < nj; ++j) {
-      const int st = j & 1;
-      if (j >= 2 && !warp_all(mbar_wait(b_ke + 8 * st, ((j >> 1) - 1) & 1, err, abort_flag))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(b_kf + 8 * st, Lay::kKVBytes);
-        mbar_arrive_expect_tx(b_vf + 8 * st, Lay::kKVBytes);
-      }
-      __syncwarp();
-      int z;
-      if (feed.mine(a, p, p.j0 + j, nd, &z)) {
-        const uint32_t off = st * Lay::kKVBytes + (lane & ((1 << feed.ppt_log2) - 1)) * (a.page_size * 128);
-#pragma unroll
-        for (int bx = 0; bx < D / 64; ++bx)
-          tma_load_3d(base + Lay::kOffK + off + bx * Lay::kBox, &tm_k, b_kf + 8 * st, 64 * bx, kvh, z);
-#pragma unroll
-        for (int bx = 0; bx < D / 64; ++bx)
-          tma_load_3d(base + Lay::kOffV + off + bx * Lay::kBox, &tm_v, b_vf + 8 * st, 64 * bx, kvh, z);
-      }
-      __syncwarp();
-    }
-    if (lane == 0 && *abort_flag && nj > 0) {
-      // every copy this CTA started lands before its shared memory is released
-      attn_drain(b_q, 0, err);
-      for (int k = j > 2 ? j - 2 : 0; k < j; ++k) {
-        attn_drain(b_kf + 8 * (k & 1), (k >> 1) & 1, err);
-        attn_drain(b_vf + 8 * (k & 1), (k >> 1) & 1, err);
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ products
-    const uint32_t idesc_s = idesc_bf16_f32(kManyRows, kKeyTile);
-    const uint32_t idesc_pv = idesc_bf16_f32(kManyRows, D) | (1u << 16);  // B (V) MN-major
-    bool ok = nj > 0 && warp_all(mbar_wait(b_q, 0, err, abort_flag));
-    auto issue_s = [&](int j) -> bool {
-      const int st = j & 1;
-      if (!warp_all(mbar_wait(b_kf + 8 * st, (j >> 1) & 1, err, abort_flag))) return false;
-      if (j >= 2 && !warp_all(mbar_wait(b_sfree + 8 * st, ((j >> 1) - 1) & 1, err, abort_flag))) return false;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t d = tmem + (st ? Lay::kColS1 : Lay::kColS0);
-        const uint32_t ks = base + Lay::kOffK + st * Lay::kKVBytes;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t qo = (kk >> 2) * kRowBox + (kk & 3) * 32;
-          const uint32_t ko = (kk >> 2) * Lay::kBox + (kk & 3) * 32;
-          umma_bf16(d, sw128_kmajor_desc(base + qo), sw128_kmajor_desc(ks + ko), idesc_s, kk > 0 ? 1u : 0u);
+            for (int bx = 0; bx < D / 64; ++bx)
+              tma_load_3d(base + h * Lay::kTile + bx * kRowBox, &tm_q, b_q, 64 * bx, p.kvh * G, p.tok0 + h * tqh);
         }
-        umma_commit(b_sf + 8 * st);
-      }
-      __syncwarp();
-      return true;
-    };
-    if (ok) ok = issue_s(0);
-    for (int j = 0; ok && j < nj; ++j) {
-      if (j + 1 < nj && !(ok = issue_s(j + 1))) break;
-      const int st = j & 1;
-      if (!warp_all(mbar_wait(b_p, j & 1, err, abort_flag)) ||
-          !warp_all(mbar_wait(b_vf + 8 * st, (j >> 1) & 1, err, abort_flag))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t vs = base + Lay::kOffV + st * Lay::kKVBytes;
+        __syncwarp();
+        ++q_loads;
+        for (int j = p.j0; ok && j < p.j1; ++j) {
+          int z;
+          const bool mine = feed.mine(a, p, j, nd, &z);
+          const uint32_t off = (lane & ((1 << feed.ppt_log2) - 1)) * (a.page_size * 128);
 #pragma unroll
-        for (int kk = 0; kk < kKeyTile / 16; ++kk)
-          umma_bf16(tmem + Lay::kColO, sw128_kmajor_desc(base + Lay::kOffP + kk * 32),
-                    sw128_mnmajor_desc(vs + kk * 2048, Lay::kBox), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(b_ke + 8 * st);
-        umma_commit(b_o);
+          for (int kv = 0; kv < 2; ++kv) {
+            if (issued >= S && !warp_all(mbar_wait(b_empty + 8 * t.at, t.ph ^ 1, err, abort_flag))) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * t.at, Lay::kTile);
+            __syncwarp();
+            if (mine) {
+              const uint32_t to = base + Lay::kOffRing + t.at * Lay::kTile + off;
+#pragma unroll
+              for (int bx = 0; bx < D / 64; ++bx)
+                tma_load_3d(to + bx * kRowBox, kv ? &tm_v : &tm_k, b_full + 8 * t.at, 64 * bx, p.kvh, z);
+            }
+            __syncwarp();
+            ++issued;
+            t.next(S);
+          }
+        }
       }
+      if (lane == 0 && *abort_flag) {
+        // every copy this CTA started lands before its shared memory is released
+        if (q_loads > 0) attn_drain(b_q, (q_loads - 1) & 1, err);
+        for (int k = 0; k < min(issued, S); ++k) {
+          if (--t.at < 0) {
+            t.at = S - 1;
+            t.ph ^= 1;
+          }
+          attn_drain(b_full + 8 * t.at, t.ph, err);
+        }
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ products
+      const uint32_t idesc_s = idesc_bf16_f32(kHalfRows, kManyKeys);
+      const uint32_t idesc_pv = idesc_bf16_f32(kHalfRows, D) | (1u << 16);  // B (V) MN-major
+      Turn t;                       // next tile of the ring to be used
+      int qn = 0, pn[2] = {0, 0};   // uses so far of q_full and p_full
+      bool ok = true;
+      for (int pi = range.x; ok && pi < range.y; ++pi) {
+        const Piece p = load_piece(a, pi);
+        const int nj = p.j1 - p.j0;
+        if (nj <= 0) continue;
+        const int halves = p.ntok > tqh ? 2 : 1;
+        if (!(ok = warp_all(mbar_wait(b_q, qn++ & 1, err, abort_flag)))) break;
+        // S_h = Q_h K^T in the place of S_h (K = D in steps of 16: 4 per 64-channel box)
+        auto issue_s = [&](int h, uint32_t ks) {
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t o = (kk >> 2) * kRowBox + (kk & 3) * 32;
+              umma_bf16(tmem + Lay::kColS + h * kManyKeys, sw128_kmajor_desc(base + h * Lay::kTile + o),
+                        sw128_kmajor_desc(ks + o), idesc_s, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(b_s + 8 * h);
+          }
+          __syncwarp();
+        };
+        auto release = [&](uint32_t bar) {
+          if (elect_one()) umma_commit(bar);
+          __syncwarp();
+        };
+        if (!(ok = warp_all(mbar_wait(b_full + 8 * t.at, t.ph, err, abort_flag)))) break;
+        tc_fence_after();
+        for (int h = 0; h < halves; ++h) issue_s(h, base + Lay::kOffRing + t.at * Lay::kTile);
+        release(b_empty + 8 * t.at);
+        if (nj == 1) release(b_qe);
+        t.next(S);
+        for (int j = 0; ok && j < nj; ++j) {
+          const Turn tv = t;
+          t.next(S);
+          const Turn tk = t;
+          if (j + 1 < nj) t.next(S);
+          if (!(ok = warp_all(mbar_wait(b_full + 8 * tv.at, tv.ph, err, abort_flag)))) break;
+          for (int h = 0; h < halves; ++h) {
+            // (weights of a piece's first tile come after O_h of the piece before has been read)
+            if (!(ok = warp_all(mbar_wait(b_p + 8 * h, pn[h]++ & 1, err, abort_flag)))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              // O_h += P_h V: K = 128 positions in steps of 16 (8 columns of P; two 8-row groups of V,
+              // the next 64 channels one box on)
+              const uint32_t vs = base + Lay::kOffRing + tv.at * Lay::kTile;
+#pragma unroll
+              for (int kk = 0; kk < kManyKeys / 16; ++kk)
+                umma_bf16_ta(tmem + Lay::kColO + h * D, tmem + Lay::kColS + h * kManyKeys + kk * 8,
+                             sw128_mnmajor_desc(vs + kk * 2048, kRowBox), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+            }
+            __syncwarp();
+            if (h == halves - 1) release(b_empty + 8 * tv.at);
+            if (j + 1 < nj) {
+              if (h == 0) {
+                if (!(ok = warp_all(mbar_wait(b_full + 8 * tk.at, tk.ph, err, abort_flag)))) break;
+                tc_fence_after();
+              }
+              issue_s(h, base + Lay::kOffRing + tk.at * Lay::kTile);
+              if (h == halves - 1) {
+                release(b_empty + 8 * tk.at);
+                if (j + 2 == nj) release(b_qe);
+              }
+            } else {
+              release(b_o + 8 * h);
+            }
+          }
+        }
+      }
+      // every product issued above completes before tensor memory is released
+      if (elect_one()) umma_commit(b_drain);
       __syncwarp();
+      attn_drain(b_drain, 0, err);
     }
-    // every product issued above completes before tensor memory is released
-    if (elect_one()) umma_commit(b_drain);
-    __syncwarp();
-    attn_drain(b_drain, 0, err);
   } else {
-    // ------------------------------------------------------------ softmax (warps 2-5), a row a thread
+    // ------------------------------------------------------------ softmax, a row a thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int h = warp >> 2;
     const int quad = warp & 3;
     const int r = quad * 32 + lane;
-    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t ts = tmem + (static_cast<uint32_t>(quad * 32) << 16) + Lay::kColS + h * kManyKeys;
+    const uint32_t to = tmem + (static_cast<uint32_t>(quad * 32) << 16) + Lay::kColO + h * D;
     const ScoreMap map = score_map(a);
-    const bool real = r < rows;
-    const int tok = real ? r / G : 0, head = kvh * G + (real ? r % G : 0);
-    const int pos = p.p0 + tok;
-    const int window = hdr.window > 0 ? hdr.window : 0x7fffffff;
-    const float slope = a.slopes != nullptr ? a.slopes[head] * kLog2e : 0.f;
     const bool mapped = a.cap > 0.f || a.slopes != nullptr;
-    // every token of the tile sees all of [sure_lo, p0]
-    const int sure_lo = hdr.window > 0 ? p.p0 + p.ntok - hdr.window : 0;
-    float m = -FLT_MAX, l = 0.f;
+    // scores enter the exponent as s * c (raw products), or as they are once mapped
+    const float c = mapped ? 1.f : a.scale_log2;
+    const float slack = kRescaleSlack / c;
+    const int rt = r / G, rg = r % G;
+    Turn tv;        // the ring's place of this key tile's V (looked at by the first half alone)
+    int sn = 0, on = 0;  // uses so far of s_full and o_full
     bool ok = true;
-    for (int j = 0; j < nj; ++j) {
-      const int st = j & 1;
-      const int k0 = key_tile(p, p.j0 + j) * kKeyTile;
-      if (!warp_all(mbar_wait(b_sf + 8 * st, (j >> 1) & 1, err, abort_flag))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      uint32_t sr[kKeyTile];
-      {
-        const uint32_t sc = tl + (st ? Lay::kColS1 : Lay::kColS0);
-        tmem_ld_32x32b_x32(sc, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-        tmem_ld_32x32b_x32(sc + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-        tmem_ld_wait();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_sfree + 8 * st);  // the accumulator may take S_{j+2}
-      if (mapped) {
-        const float d0 = static_cast<float>(k0 - pos);
-#pragma unroll
-        for (int k = 0; k < kKeyTile; ++k)
-          sr[k] = __float_as_uint(fmaf(slope, d0 + static_cast<float>(k), map(__uint_as_float(sr[k]))));
-      } else {
-#pragma unroll
-        for (int k = 0; k < kKeyTile; ++k) sr[k] = __float_as_uint(__uint_as_float(sr[k]) * map.scale);
-      }
-      if (!(k0 >= sure_lo && k0 + kKeyTile - 1 <= p.p0)) {
-        // visible: k <= hi and k > lo, or in the prefix (offsets into the tile)
-        const int hi = real ? pos - k0 : -1, lo = real ? (window == 0x7fffffff ? -1 : pos - window - k0) : 0x7fffffff;
-        const int pre = real ? p.pre - k0 : 0;
-#pragma unroll
-        for (int k = 0; k < kKeyTile; ++k)
-          if (!((k <= hi && k > lo) || k < pre)) sr[k] = __float_as_uint(-FLT_MAX);
-      }
-      float mx4[4] = {m, -FLT_MAX, -FLT_MAX, -FLT_MAX};
-#pragma unroll
-      for (int k = 0; k < kKeyTile; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], __uint_as_float(sr[k]));
-      float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-      // the row keeps its reference maximum until the tile's exceeds it by kRescaleSlack: weights
-      // then stay below 2^kRescaleSlack, and O is rescaled only when some row moves its reference
-      if (mx <= m + kRescaleSlack) mx = m;
-      const float ref = mx == -FLT_MAX ? 0.f : mx;  // no visible key yet: hidden keys weigh zero
-      const float corr = exp2_approx(__fsub_rn(m, mx));
-      const bool partial = !nd.all(k0, k0 + kKeyTile);
-      if (j > 0) {
-        // P_{j-1} V_{j-1} has landed: O may be rescaled and the P buffer rewritten
-        if (!warp_all(mbar_wait(b_o, (j - 1) & 1, err, abort_flag))) {
+    for (int pi = range.x; ok && pi < range.y; ++pi) {
+      const Piece p = load_piece(a, pi);
+      const int nj = p.j1 - p.j0;
+      const int tok = h * tqh + rt;
+      if (h == 1 && p.ntok <= tqh) continue;
+      const Needed nd = needed_keys(p, hdr.window);
+      const bool real = rt < tqh && tok < p.ntok;
+      const int head = p.kvh * G + rg;
+      const int pos = p.p0 + tok;
+      const float slope = a.slopes != nullptr ? a.slopes[head] * kLog2e : 0.f;
+      // every token of the half sees all of [sure_lo, sure_hi]
+      const int sure_hi = p.p0 + h * tqh;
+      const int sure_lo = hdr.window > 0 ? p.p0 + min(p.ntok, (h + 1) * tqh) - hdr.window : 0;
+      float m = -FLT_MAX, l = 0.f;
+      for (int j = 0; j < nj; ++j) {
+        const int k0 = key_tile(p, p.j0 + j) * kManyKeys;
+        tv.next(S);  // past K
+        if (!warp_all(mbar_wait(b_s + 8 * h, sn++ & 1, err, abort_flag))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (__any_sync(0xffffffffu, corr != 1.f ? 1 : 0)) {
+        uint32_t sr[kManyKeys];
+#pragma unroll
+        for (int cc = 0; cc < kManyKeys / 32; ++cc)
+          tmem_ld_32x32b_x32(ts + 32 * cc, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * cc]));
+        tmem_ld_wait();
+        if (mapped) {
+          const float d0 = static_cast<float>(k0 - pos);
+#pragma unroll
+          for (int k = 0; k < kManyKeys; ++k)
+            sr[k] = __float_as_uint(fmaf(slope, d0 + static_cast<float>(k), map(__uint_as_float(sr[k]))));
+        }
+        if (!(k0 >= sure_lo && k0 + kManyKeys - 1 <= sure_hi)) {
+          // visible: lo < k <= hi, or in the prefix (offsets into the tile)
+          const int hi = real ? pos - k0 : -1, lo = hdr.window > 0 ? pos - hdr.window - k0 : -1;
+          const int pre = real ? p.pre - k0 : 0;
+#pragma unroll
+          for (int k = 0; k < kManyKeys; ++k)
+            if (!((k <= hi && k > lo) || k < pre)) sr[k] = __float_as_uint(-FLT_MAX);
+        }
+        float mx4[4] = {m, -FLT_MAX, -FLT_MAX, -FLT_MAX};
+#pragma unroll
+        for (int k = 0; k < kManyKeys; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], __uint_as_float(sr[k]));
+        float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        // the row keeps its reference maximum until the tile's exceeds it by the slack: weights then
+        // stay below 2^kRescaleSlack, and O is rescaled only when some row moves its reference
+        if (mx <= m + slack) mx = m;
+        const float corr = real ? exp2_approx((m - mx) * c) : 1.f;  // (rows that are not there hold anything)
+        // (S_j complete means P_{j-1} V_{j-1} complete: the products of a half run in order)
+        if (j > 0 && __any_sync(0xffffffffu, corr != 1.f ? 1 : 0)) {
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t o[32];
-            tmem_ld_32x32b_x32(tl + Lay::kColO + 32 * cc, o);
+            tmem_ld_32x32b_x32(to + 32 * cc, o);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__fmul_rn(__uint_as_float(o[e]), corr));
-            tmem_st_32x32b_x32(tl + Lay::kColO + 32 * cc, o);
+            tmem_st_32x32b_x32(to + 32 * cc, o);
           }
-          tmem_st_wait();
         }
+        if (h == 0 && !nd.all(k0, k0 + kManyKeys)) {
+          // rows of V that no token sees may hold anything: their weight is zero, so make them zero
+          // (the products of both halves wait for the first half's weights)
+          if (!warp_all(mbar_wait(b_full + 8 * tv.at, tv.ph, err, abort_flag))) {
+            ok = false;
+            break;
+          }
+          if (!nd.at(k0 + r)) {
+            const uint32_t vr = base + Lay::kOffRing + tv.at * Lay::kTile + r * 128;
+#pragma unroll
+            for (int bx = 0; bx < D / 64; ++bx)
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vr + bx * kRowBox + q * 16), "r"(0)
+                             : "memory");
+          }
+          fence_proxy_async_smem();
+        }
+        // P = exp2((s - m) c) in the place of S; no visible key yet: a reference of zero keeps the
+        // weights of hidden keys at zero
+        const float ref = mx == -FLT_MAX ? 0.f : -mx * c;
+        float rs4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int cc = 0; cc < kManyKeys / 64; ++cc) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float p0 = exp2_approx(fmaf(__uint_as_float(sr[64 * cc + 2 * e]), c, ref));
+            const float p1 = exp2_approx(fmaf(__uint_as_float(sr[64 * cc + 2 * e + 1]), c, ref));
+            w[e] = pack_bf16x2(p0, p1);
+            rs4[e & 3] += bf16lo_to_f32(w[e]) + bf16hi_to_f32(w[e]);
+          }
+          tmem_st_32x32b_x32(ts + 32 * cc, w);
+        }
+        l = fmaf(l, corr, (rs4[0] + rs4[1]) + (rs4[2] + rs4[3]));
+        m = mx;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_p + 8 * h);
+        tv.next(S);  // past V
       }
-      if (partial) {
-        // rows of V that no token sees may hold anything: their weight is zero, so make them zero
-        if (!warp_all(mbar_wait(b_vf + 8 * st, (j >> 1) & 1, err, abort_flag))) {
-          ok = false;
-          break;
-        }
-        if (!nd.at(k0 + (r >> 1))) {
-          const uint32_t vr = base + Lay::kOffV + st * Lay::kKVBytes + (r >> 1) * 128 + (r & 1) * 64;
-#pragma unroll
-          for (int bx = 0; bx < D / 64; ++bx)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vr + bx * Lay::kBox + c * 16), "r"(0)
-                           : "memory");
-        }
+      if (!ok || (nj > 0 && !warp_all(mbar_wait(b_o + 8 * h, on++ & 1, err, abort_flag)))) {
+        ok = false;
+        break;
       }
-      float rs4[4] = {0.f, 0.f, 0.f, 0.f};  // the row sum as four chains, added in a fixed order
-      const uint32_t prow = base + Lay::kOffP + r * 128;
-#pragma unroll
-      for (int k8 = 0; k8 < kKeyTile / 8; ++k8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p0 = exp2_approx(__fsub_rn(__uint_as_float(sr[8 * k8 + 2 * e]), ref));
-          const float p1 = exp2_approx(__fsub_rn(__uint_as_float(sr[8 * k8 + 2 * e + 1]), ref));
-          w[e] = pack_bf16x2(p0, p1);
-          rs4[e] = __fadd_rn(rs4[e], __fadd_rn(bf16lo_to_f32(w[e]), bf16hi_to_f32(w[e])));
-        }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(prow + ((k8 ^ (r & 7)) << 4)), "r"(w[0]),
-                     "r"(w[1]), "r"(w[2]), "r"(w[3])
-                     : "memory");
-      }
-      const float rs = __fadd_rn(__fadd_rn(rs4[0], rs4[1]), __fadd_rn(rs4[2], rs4[3]));
-      l = __fmaf_rn(l, corr, rs);
-      m = mx;
-      fence_proxy_async_smem();  // the tensor cores read P (and V) through the async proxy
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_p);
-    }
-    if (ok && (nj == 0 || warp_all(mbar_wait(b_o, (nj - 1) & 1, err, abort_flag)))) {
       tc_fence_after();
       const float inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
       __nv_bfloat16* orow = a.out + static_cast<int64_t>(p.tok0 + tok) * a.ld_out + head * D;
-      const int64_t prow = (static_cast<int64_t>(p.slot) * hdr.kv_heads + kvh) * a.row_cap + r;
+      const int64_t prow = static_cast<int64_t>(p.slot) * a.row_cap + h * kHalfRows + r;
 #pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t o[32];
         if (nj > 0) {
-          tmem_ld_32x32b_x32(tl + Lay::kColO + 32 * cc, o);
+          tmem_ld_32x32b_x32(to + 32 * cc, o);
           tmem_ld_wait();
         } else {
 #pragma unroll
@@ -1015,73 +1139,91 @@ __global__ void __launch_bounds__(kManyThreads, 2)
           for (int q4 = 0; q4 < 8; ++q4)
             *reinterpret_cast<uint4*>(a.acc + prow * D + 32 * cc + 4 * q4) =
                 make_uint4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
-          if (cc == 0) a.ml[prow] = make_float2(m, l);
+          if (cc == 0) a.ml[prow] = make_float2(mapped ? m : m * c, l);
         }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 9) {
     tc_fence_after();
-    tmem_dealloc(tmem, Lay::kTmemCols);
+    tmem_dealloc(tmem, 512);
   }
 }
 
 // ---------------------------------------------------------------- joining the pieces of a tile
 
-// A block per (split tile, key/value head, row): the warps take every eighth piece, then join.
-template <int D>
+// Blocks walk the rows of the split tiles. TEAM (few rows, possibly many pieces): a row a block,
+// every warp taking every eighth piece, then joined; else a row a warp.
+template <int D, bool TEAM>
 __global__ void __launch_bounds__(256) merge_kernel(const PagedArgs a) {
   constexpr int E = D / 32;
   using Vec = typename std::conditional<E == 4, float4, float2>::type;
   __shared__ float m_sh[8], l_sh[8];
-  __shared__ float acc_sh[8][D];
+  __shared__ float acc_sh[TEAM ? 8 : 1][D];
   pdl_enter();
   const PlanHeader hdr = *reinterpret_cast<const PlanHeader*>(a.plan);
   if (!plan_ok(hdr, a.want)) return;
-  const int kvh = static_cast<int>(blockIdx.x) % hdr.kv_heads;
-  const int si = static_cast<int>(blockIdx.x) / hdr.kv_heads;
-  if (si >= hdr.splits) return;
-  const Split s = reinterpret_cast<const Split*>(a.plan + a.off_splits)[si];
-  const int r = blockIdx.y;
-  if (r >= s.ntok * a.G) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t step = static_cast<int64_t>(hdr.kv_heads) * a.row_cap;
-  const int64_t row = (static_cast<int64_t>(s.slot0) * hdr.kv_heads + kvh) * a.row_cap + r;
-  float M = -FLT_MAX;
-  for (int i = threadIdx.x; i < s.pieces; i += 256) M = fmaxf(M, a.ml[row + i * step].x);
+  const int per = TEAM ? 1 : 8;  // rows a block takes at once
+  const int steps = (a.row_cap + per - 1) / per;
+  for (int64_t w = blockIdx.x; w < static_cast<int64_t>(hdr.splits) * steps; w += gridDim.x) {
+    const Split s = reinterpret_cast<const Split*>(a.plan + a.off_splits)[w / steps];
+    const int r = static_cast<int>(w % steps) * per + (TEAM ? 0 : warp);
+    // the row's token and head (rows of a tcgen05 half are padded to kHalfRows)
+    const int half = TEAM ? 0 : r / kHalfRows, rr = TEAM ? r : r % kHalfRows;
+    const int tqh = kHalfRows / a.G;
+    const int tok = half * tqh + rr / a.G;
+    if (tok >= s.ntok || (!TEAM && rr / a.G >= tqh)) continue;  // (the same for all that meet below)
+    const int64_t row = static_cast<int64_t>(s.slot0) * a.row_cap + r;
+    const int first = TEAM ? warp : 0, step = TEAM ? 8 : 1;
+    float M = -FLT_MAX;
+    for (int i = TEAM ? threadIdx.x : lane; i < s.pieces; i += TEAM ? 256 : 32)
+      M = fmaxf(M, a.ml[row + static_cast<int64_t>(i) * a.row_cap].x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) m_sh[warp] = M;
-  __syncthreads();
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (TEAM) {
+      if (lane == 0) m_sh[warp] = M;
+      __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 8; ++w) M = fmaxf(M, m_sh[w]);
-  float acc[E], l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < s.pieces; i += 8) {
-    const float2 ml = a.ml[row + i * step];
-    const float f = exp2_approx(ml.x - M);
-    Vec v = *reinterpret_cast<const Vec*>(a.acc + (row + i * step) * D + lane * E);
-    l = fmaf(ml.y, f, l);
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(reinterpret_cast<const float*>(&v)[e], f, acc[e]);
-  }
-  if (lane == 0) l_sh[warp] = l;
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc_sh[warp][lane * E + e] = acc[e];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float ls = 0.f, v = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      ls += l_sh[w];
-      v += acc_sh[w][threadIdx.x];
+      for (int i = 0; i < 8; ++i) M = fmaxf(M, m_sh[i]);
     }
-    a.out[static_cast<int64_t>(s.tok0 + r / a.G) * a.ld_out + (kvh * a.G + r % a.G) * D + threadIdx.x] =
-        __float2bfloat16_rn(ls > 0.f ? __fdiv_rn(v, ls) : 0.f);
+    float acc[E], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int i = first; i < s.pieces; i += step) {
+      const int64_t at = row + static_cast<int64_t>(i) * a.row_cap;
+      const float2 ml = a.ml[at];
+      const float f = exp2_approx(ml.x - M);
+      const Vec v = *reinterpret_cast<const Vec*>(a.acc + at * D + lane * E);
+      l = fmaf(ml.y, f, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(reinterpret_cast<const float*>(&v)[e], f, acc[e]);
+    }
+    __nv_bfloat16* dst = a.out + static_cast<int64_t>(s.tok0 + tok) * a.ld_out + (s.kvh * a.G + rr % a.G) * D;
+    if (TEAM) {
+      if (lane == 0) l_sh[warp] = l;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc_sh[warp][lane * E + e] = acc[e];
+      __syncthreads();
+      if (threadIdx.x < D) {
+        float ls = 0.f, v = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          ls += l_sh[i];
+          v += acc_sh[i][threadIdx.x];
+        }
+        dst[threadIdx.x] = __float2bfloat16_rn(ls > 0.f ? __fdiv_rn(v, ls) : 0.f);
+      }
+      __syncthreads();  // the exchange is rewritten by the next row
+    } else {
+      const float inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
+#pragma unroll
+      for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t*>(dst + lane * E + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    }
   }
 }
 
@@ -1105,33 +1247,35 @@ cudaError_t prepare_kernel(K kernel, size_t smem) {
 }
 
 template <int D>
-cudaError_t launch_attention_d(const PagedArgs& a, const PagedShape& s, const PagePool& p, const PlanLayout& l,
+cudaError_t launch_attention_d(PagedArgs a, const PagedShape& s, const PagePool& p, const PlanLayout& l, int num_sms,
                                cudaStream_t stream) {
   const uint64_t positions = static_cast<uint64_t>(p.num_pages) * p.page_size;
   const uint64_t s1 = D * 2, s2 = static_cast<uint64_t>(s.kv_heads) * D * 2;
-  const uint32_t box = static_cast<uint32_t>(std::min<int64_t>(p.page_size, kKeyTile));
+  const uint32_t box = static_cast<uint32_t>(std::min<int64_t>(p.page_size, l.key_tile));
   CUtensorMap tk, tv;
   if (!encode_bf16_tmap_3d(&tk, p.k, D, s.kv_heads, positions, s1, s2, 64, 1, box) ||
       !encode_bf16_tmap_3d(&tv, p.v, D, s.kv_heads, positions, s1, s2, 64, 1, box))
     return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(l.max_pieces * s.kv_heads));
+  const dim3 grid(static_cast<unsigned>(l.ctas));
   cudaError_t e;
   if (l.rows == kFewRows) {
-    e = prepare_kernel(few_rows_kernel<D>, FewLayout<D>::kSmem);
-    if (e == cudaSuccess)
-      e = launch_pdl(few_rows_kernel<D>, grid, dim3(kFewThreads), FewLayout<D>::kSmem, stream, tk, tv, a);
-  } else {
-    CUtensorMap tq;
-    if (!encode_bf16_tmap_3d(&tq, a.q, D, s.heads, s.tokens, D * 2, static_cast<uint64_t>(a.ld_q) * 2, 64,
-                             static_cast<uint32_t>(a.G), static_cast<uint32_t>(l.tq)))
-      return cudaErrorInvalidValue;
-    e = prepare_kernel(many_rows_kernel<D>, ManyLayout<D>::kSmem);
-    if (e == cudaSuccess)
-      e = launch_pdl(many_rows_kernel<D>, grid, dim3(kManyThreads), ManyLayout<D>::kSmem, stream, tq, tk, tv, a);
+    const size_t smem = FewLayout<D>::smem(l.row_cap);
+    a.stages = FewLayout<D>::stages(l.row_cap);
+    e = prepare_kernel(few_rows_kernel<D>, smem);
+    if (e == cudaSuccess) e = launch_pdl(few_rows_kernel<D>, grid, dim3(kFewThreads), smem, stream, tk, tv, a);
+    if (e != cudaSuccess) return e;
+    const int blocks = std::min(l.max_splits * l.row_cap, num_sms * 8);
+    return launch_pdl(merge_kernel<D, true>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, a);
   }
-  if (e != cudaSuccess || l.max_splits == 0) return e;
-  return launch_pdl(merge_kernel<D>, dim3(static_cast<unsigned>(l.max_splits * s.kv_heads), l.row_cap), dim3(256), 0,
-                    stream, a);
+  CUtensorMap tq;
+  if (!encode_bf16_tmap_3d(&tq, a.q, D, s.heads, s.tokens, D * 2, static_cast<uint64_t>(a.ld_q) * 2, 64,
+                           static_cast<uint32_t>(a.G), static_cast<uint32_t>(kHalfRows / a.G)))
+    return cudaErrorInvalidValue;
+  e = prepare_kernel(many_rows_kernel<D>, ManyLayout<D>::kSmem);
+  if (e == cudaSuccess)
+    e = launch_pdl(many_rows_kernel<D>, grid, dim3(kManyThreads), ManyLayout<D>::kSmem, stream, tq, tk, tv, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(merge_kernel<D, false>, dim3(static_cast<unsigned>(num_sms * 8)), dim3(256), 0, stream, a);
 }
 
 }  // namespace
@@ -1151,6 +1295,7 @@ cudaError_t launch_paged_attention(const void* q, int64_t ld_q, const PagedShape
   PagedArgs a = {};
   a.want = plan_header(s, 0);
   a.plan = static_cast<const uint8_t*>(plan);
+  a.off_cta = l.off_cta;
   a.off_pieces = l.off_pieces;
   a.off_splits = l.off_splits;
   a.acc = reinterpret_cast<float*>(static_cast<uint8_t*>(plan) + l.off_acc);
@@ -1171,7 +1316,8 @@ cudaError_t launch_paged_attention(const void* q, int64_t ld_q, const PagedShape
   a.ld_out = static_cast<int>(s.heads * s.head_dim);
   a.out = static_cast<__nv_bfloat16*>(out);
   a.err = err;
-  return s.head_dim == 64 ? launch_attention_d<64>(a, s, p, l, stream) : launch_attention_d<128>(a, s, p, l, stream);
+  return s.head_dim == 64 ? launch_attention_d<64>(a, s, p, l, num_sms, stream)
+                          : launch_attention_d<128>(a, s, p, l, num_sms, stream);
 }
 
 }  // namespace ttq
