@@ -556,6 +556,7 @@ class _OnDevice:
         if torch.cuda.current_device() != self.index:
             self.guard = torch.cuda.device(self.index)
             self.guard.__enter__()
+        return self
 
     def __exit__(self, *exc):
         if self.guard is not None:
@@ -580,6 +581,15 @@ def _same_device(*named):
         elif at != index:
             raise ValueError(f"{name} is on cuda:{at}, the other tensors on cuda:{index}")
     return _OnDevice(index)
+
+
+def _queue(stream, guard):
+    """Handle of the given stream, or of the current one of the guarded device."""
+    if stream is not None:
+        return stream.cuda_stream
+    from torch._C import _cuda_getCurrentRawStream
+
+    return _cuda_getCurrentRawStream(guard.index)
 
 
 def _address(t, dtype, name):
@@ -640,11 +650,11 @@ class AttentionPlan:
         _shape(q_start, "q_start", (self.seqs + 1,))
         _shape(kv_len, "kv_len", (self.seqs,))
         _shape(prefix, "prefix", (self.seqs,))
-        with _same_device(("q_start", q_start), ("kv_len", kv_len), ("prefix", prefix), ("plan", self.buffer)):
+        with _same_device(("q_start", q_start), ("kv_len", kv_len), ("prefix", prefix), ("plan", self.buffer)) as on:
             _check("ttq_attention_plan", load_library().ttq_attention_plan(
                 _address(q_start, int32, "q_start"), _address(kv_len, int32, "kv_len"),
                 _address(prefix, int32, "prefix"), window, self.seqs, self.tokens, self.max_new, self.heads,
-                self.kv_heads, self.head_dim, self.buffer.data_ptr(), self.buffer.numel(), _stream(stream)))
+                self.kv_heads, self.head_dim, self.buffer.data_ptr(), self.buffer.numel(), _queue(stream, on)))
         return self
 
 
@@ -666,14 +676,14 @@ def paged_attention(q, plan: AttentionPlan, k_pages, v_pages, page_table, softca
     if q.dtype != bfloat16:
         raise TypeError(f"q must be {bfloat16}, got {q.dtype}")
     with _same_device(("q", q), ("k_pages", k_pages), ("v_pages", v_pages), ("page_table", page_table),
-                      ("slopes", slopes), ("out", out), ("plan", plan.buffer)):
+                      ("slopes", slopes), ("out", out), ("plan", plan.buffer)) as on:
         if out is None:
             out = q.new_empty((T, H * D))
         _check("ttq_paged_attention", load_library().ttq_paged_attention(
             q.data_ptr(), q.stride(0) if T > 1 else q.shape[1], plan.seqs, T, plan.max_new, H, plan.kv_heads, D,
             _address(k_pages, bfloat16, "k_pages"), _address(v_pages, bfloat16, "v_pages"), pages, page_size,
             _address(page_table, int32, "page_table"), width, softcap, _address(slopes, float32, "slopes"),
-            _address(out, bfloat16, "out"), plan.buffer.data_ptr(), plan.buffer.numel(), _stream(stream)))
+            _address(out, bfloat16, "out"), plan.buffer.data_ptr(), plan.buffer.numel(), _queue(stream, on)))
     return out
 
 
@@ -697,7 +707,7 @@ def qk_norm_rope_paged(qkv, heads: int, kv_heads: int, head_dim: int, q_norm, k_
     _shape(q, "q", (T, heads * head_dim))
     with _same_device(("qkv", qkv), ("q_norm", q_norm), ("k_norm", k_norm), ("table", table), ("q_start", q_start),
                       ("kv_len", kv_len), ("k_pages", k_pages), ("v_pages", v_pages), ("page_table", page_table),
-                      ("q", q)):
+                      ("q", q)) as on:
         if q is None:
             q = qkv.new_empty((T, heads * head_dim))
         _check("ttq_qk_norm_rope_paged", load_library().ttq_qk_norm_rope_paged(
@@ -705,7 +715,7 @@ def qk_norm_rope_paged(qkv, heads: int, kv_heads: int, head_dim: int, q_norm, k_
             _address(k_norm, bfloat16, "k_norm"), eps, _address(table, float32, "table"), table.shape[0],
             _address(q_start, int32, "q_start"), _address(kv_len, int32, "kv_len"),
             _address(k_pages, bfloat16, "k_pages"), _address(v_pages, bfloat16, "v_pages"), pages, page_size,
-            _address(page_table, int32, "page_table"), width, _address(q, bfloat16, "q"), _stream(stream)))
+            _address(page_table, int32, "page_table"), width, _address(q, bfloat16, "q"), _queue(stream, on)))
     return q
 
 
@@ -725,12 +735,12 @@ def copy_pages(k_pool, v_pool, src, dst, stream=None):
     _shape(dst, "dst", tuple(src.shape))
     layers = shape[0] if len(shape) == 5 else 1
     page_bytes = shape[-3] * shape[-2] * shape[-1] * k_pool.element_size()
-    with _same_device(("k_pool", k_pool), ("v_pool", v_pool), ("src", src), ("dst", dst)):
+    with _same_device(("k_pool", k_pool), ("v_pool", v_pool), ("src", src), ("dst", dst)) as on:
         if src.shape[0] == 0:
             return
         _check("ttq_copy_pages", load_library().ttq_copy_pages(
             _address(k_pool, k_pool.dtype, "k_pool"), _address(v_pool, k_pool.dtype, "v_pool"), layers, shape[-4],
-            page_bytes, _address(src, int32, "src"), _address(dst, int32, "dst"), src.shape[0], _stream(stream)))
+            page_bytes, _address(src, int32, "src"), _address(dst, int32, "dst"), src.shape[0], _queue(stream, on)))
 
 
 def remap_pages(table, mapping, out=None, stream=None):
@@ -741,12 +751,12 @@ def remap_pages(table, mapping, out=None, stream=None):
     if mapping.dim() != 1:
         raise ValueError("mapping holds one entry a page")
     _shape(out, "out", tuple(table.shape))
-    with _same_device(("table", table), ("mapping", mapping), ("out", out)):
+    with _same_device(("table", table), ("mapping", mapping), ("out", out)) as on:
         if out is None:
             out = table.new_empty(table.shape)
         _check("ttq_remap_pages", load_library().ttq_remap_pages(
             _address(table, int32, "table"), table.numel(), _address(mapping, int32, "mapping"), mapping.shape[0],
-            _address(out, int32, "out"), _stream(stream)))
+            _address(out, int32, "out"), _queue(stream, on)))
     return out
 
 
@@ -765,7 +775,7 @@ def token_logprobs(logits, tokens, top: int = 0, ws=None, stream=None):
     kind = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(logits.dtype)
     if kind is None:
         raise TypeError(f"logits must be bf16, fp16 or fp32, got {logits.dtype}")
-    with _same_device(("logits", logits), ("tokens", tokens), ("ws", ws)):
+    with _same_device(("logits", logits), ("tokens", tokens), ("ws", ws)) as on:
         lib = load_library()
         n = ctypes.c_size_t(0)
         _check("ttq_token_logprobs_workspace_size",
@@ -783,5 +793,5 @@ def token_logprobs(logits, tokens, top: int = 0, ws=None, stream=None):
             _address(tokens, torch.int64, "tokens"), top, out["logprob"].data_ptr(), out["entropy"].data_ptr(),
             None if ids is None else ids.data_ptr(), None if lps is None else lps.data_ptr(),
             None if ws is None else _address(ws, ws.dtype, "ws"), 0 if ws is None else ws.numel() * ws.element_size(),
-            _stream(stream)))
+            _queue(stream, on)))
     return out

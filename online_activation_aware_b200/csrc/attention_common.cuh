@@ -1,5 +1,6 @@
 // Device helpers shared by the attention kernels on the tensor cores: 3-D TMA loads, stores to
-// tensor memory, the MN-major operand descriptor, the fast power of two and bounded drains.
+// tensor memory, the MN-major operand descriptor, the fast power of two, packed fp32 arithmetic
+// and bounded drains.
 #pragma once
 
 #include "ttq_common.cuh"
@@ -62,5 +63,29 @@ __device__ __forceinline__ void attn_drain(uint32_t bar, uint32_t parity, const 
 
 // The predicate agreed by the whole warp.
 __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v ? 1 : 0) != 0; }
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
+  return a;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
+  return a;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+  return c;
+}
 
 }  // namespace ttq

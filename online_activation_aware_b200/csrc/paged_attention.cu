@@ -17,7 +17,7 @@
 //   many_rows_kernel tiles of up to 256 rows on tcgen05;
 //   merge_kernel     joins the pieces of a split tile.
 // Scores, maxima, sums and accumulators are fp32; the weights are rounded to bf16 for the second
-// product, and the sums add the rounded weights, so that the normalisation matches them.
+// product.
 // Every mbarrier wait is bounded: a CTA that gives up records TTQ_ERR_TIMEOUT, drains what it
 // started and returns.
 #include <algorithm>
@@ -137,40 +137,42 @@ __device__ __forceinline__ TileKeys tile_keys(int p0, int ntok, int pre, int win
 // as two key tiles.
 __device__ __forceinline__ int tile_cost(int total) { return total + 2; }
 
-// Exclusive scan over the block (kPlanThreads threads); *total gets the sum.
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* total, uint64_t* sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t x = v;
+__device__ __forceinline__ uint64_t warp_scan(uint64_t x) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    if ((threadIdx.x & 31) >= o) x += y;
   }
-  if (lane == 31) sh[warp] = x;
+  return x;
+}
+// Exclusive scan over the block (kPlanThreads threads); *total gets the sum. `turn` alternates
+// between calls, so that one barrier a call is enough.
+__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* total, uint64_t (&sh)[2][32], int& turn) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint64_t x = warp_scan(v);
+  if (lane == 31) sh[turn][warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    uint64_t w = sh[lane];
-    const uint64_t own = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    sh[lane] = w - own;
-    if (lane == 31) sh[32] = w;
-  }
-  __syncthreads();
-  const uint64_t r = sh[warp] + x - v;
-  *total = sh[32];
-  __syncthreads();  // sh is reused
-  return r;
+  const uint64_t w = warp_scan(sh[turn][lane]);
+  turn ^= 1;
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const uint64_t before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  return (warp > 0 ? before : 0) + x - v;
+}
+
+// floor(a / d) with inv = 1 / d (exact: the estimate is off by one at most).
+__device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t d, double inv) {
+  uint64_t q = static_cast<uint64_t>(static_cast<double>(a) * inv);
+  if (q * d > a) --q;
+  if ((q + 1) * d <= a) ++q;
+  return q;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restrict__ q_start,
                                                            const int* __restrict__ kv_len,
                                                            const int* __restrict__ prefix, PlanHeader h, PlanLayout l,
                                                            uint8_t* plan, unsigned* err) {
-  __shared__ uint64_t sh[33];
+  __shared__ uint64_t sh[2][32];
+  int turn = 0;
   __shared__ int2 tile_seq_sh[kPlanTiles];
   __shared__ uint64_t tile_at_sh[kPlanTiles];
   pdl_enter();
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
     const int b = b0 + tid;
     const int n = b < h.seqs ? q_start[b + 1] - q_start[b] : 0;
     uint64_t tot;
-    const int at = static_cast<int>(sum + block_scan((n + l.tq - 1) / l.tq, &tot, sh));
+    const int at = static_cast<int>(sum + block_scan((n + l.tq - 1) / l.tq, &tot, sh, turn));
     for (int i = 0; i * l.tq < n; ++i) tile_seq[at + i] = make_int2(b, i * l.tq);
     sum += tot;
   }
@@ -232,13 +234,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
       Piece p;
       cost = static_cast<uint64_t>(tile_cost(tile_of(t, &p).total)) * h.kv_heads;
     }
-    const uint64_t at = work + block_scan(cost, &tot, sh);
+    const uint64_t at = work + block_scan(cost, &tot, sh, turn);
     if (t < ntiles) tile_at[t] = at;
     work += tot;
   }
   __syncthreads();
   // equal shares; a share shorter than a few key tiles is not worth its start
   const uint64_t share = max(static_cast<uint64_t>(4), (work + l.ctas - 1) / l.ctas);
+  const double inv_share = 1.0 / static_cast<double>(share);
   // pieces of every item (tile, kv head), scanned as (pieces, slots, splits) in 32 + 16 + 16 bits
   const int items = ntiles * h.kv_heads;
   uint64_t base = 0;
@@ -254,19 +257,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
       k = tile_of(t, &p);
       cost = tile_cost(k.total);
       a = tile_at[t] + static_cast<uint64_t>(p.kvh) * cost;
-      c0 = a / share;
-      np = static_cast<int>((a + cost - 1) / share - c0) + 1;
+      c0 = divide(a, share, inv_share);
+      np = static_cast<int>(divide(a + cost - 1, share, inv_share) - c0) + 1;
       v = static_cast<uint64_t>(np) << 32 | (np > 1 ? static_cast<uint64_t>(np) << 16 | 1u : 0u);
     }
-    const uint64_t here = base + block_scan(v, &tot, sh);
+    const uint64_t here = base + block_scan(v, &tot, sh, turn);
     base += tot;
     const int first = static_cast<int>(here >> 32), slot0 = static_cast<int>(here >> 16 & 0xffff);
     const int split = static_cast<int>(here & 0xffff);
     if (np > 1 && split < l.max_splits) splits[split] = Split{p.tok0, p.ntok, slot0, np, p.kvh, {0, 0, 0}};
+    const float keys = static_cast<float>(k.total) / static_cast<float>(cost);  // key tiles per unit
+    auto key_at = [&](int x) { return x == cost ? k.total : min(k.total, static_cast<int>(static_cast<float>(x) * keys)); };
     for (int n = 0; n < np; ++n) {
       const uint64_t lo = max(a, (c0 + n) * share) - a, hi = min(a + cost, (c0 + n + 1) * share) - a;
-      p.j0 = static_cast<int>(lo * k.total / cost);
-      p.j1 = static_cast<int>(hi * k.total / cost);
+      p.j0 = key_at(static_cast<int>(lo));
+      p.j1 = key_at(static_cast<int>(hi));
       p.slot = np > 1 ? slot0 + n : -1;
       if (first + n < l.max_pieces) pieces[first + n] = p;
       if (a + lo == (c0 + n) * share) cta_first[c0 + n] = first + n;  // (c0 + n < ctas: share covers the work)
@@ -779,6 +784,92 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, u
       : "memory");
 }
 
+// 2^y for -126 <= y < 128 on the FMA pipes: y = n + f with n the nearest integer (Cody and Waite's
+// reduction, by adding and taking away 1.5 * 2^23), 2^f by the cubic of least relative error on
+// [-1/2, 1/2] (7.5e-5, against the 2^-8 that a weight loses when it is rounded to bf16), n added to
+// the exponent. Two at once.
+__device__ __forceinline__ float2 exp2_fma2(uint64_t y) {
+  const uint64_t magic = pack2(12582912.f, 12582912.f), minus = pack2(-12582912.f, -12582912.f);
+  const uint64_t t = add2(y, magic);
+  const uint64_t f = fma2(add2(t, minus), pack2(-1.f, -1.f), y);
+  uint64_t p = fma2(f, pack2(0.0551716685f, 0.0551716685f), pack2(0.2426111251f, 0.2426111251f));
+  p = fma2(p, f, pack2(0.6932609677f, 0.6932609677f));
+  p = fma2(p, f, pack2(0.9999280572f, 0.9999280572f));
+  const float2 tt = unpack2(t), pp = unpack2(p);
+  return make_float2(__int_as_float(__float_as_int(pp.x) + (__float_as_int(tt.x) << 23)),
+                     __int_as_float(__float_as_int(pp.y) + (__float_as_int(tt.y) << 23)));
+}
+
+// A row's weights 2^(s c + ref), rounded to bf16 and stored over its scores in tensor memory;
+// returns their sum (before the rounding, whose errors average out over the row).
+// SURE: every score is a real one, so a fourth of the weights can go to exp2_fma2: the special
+// function unit takes eight cycles for a warp's exponentials, and with two warps on each it would
+// need all the time that the tensor cores do.
+template <bool SURE>
+__device__ __forceinline__ float weights(uint32_t (&sr)[kManyKeys], float c, float ref, uint32_t ts) {
+  const uint64_t c2 = pack2(c, c), ref2 = pack2(ref, ref);
+  uint64_t sum[2] = {0, 0};
+#pragma unroll
+  for (int cc = 0; cc < kManyKeys / 64; ++cc) {
+    uint32_t w[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      uint64_t y2 = fma2(pack2(__uint_as_float(sr[64 * cc + 2 * e]), __uint_as_float(sr[64 * cc + 2 * e + 1])), c2, ref2);
+      float2 y = unpack2(y2);
+      if (SURE && (e & 3) == 3) {
+        y = exp2_fma2(pack2(fmaxf(y.x, -126.f), fmaxf(y.y, -126.f)));
+      } else {
+        y.x = exp2_approx(y.x);
+        y.y = exp2_approx(y.y);
+      }
+      w[e] = pack_bf16x2(y.x, y.y);
+      sum[e & 1] = add2(sum[e & 1], pack2(y.x, y.y));
+    }
+    tmem_st_32x32b_x32(ts + 32 * cc, w);
+  }
+  const float2 s = unpack2(add2(sum[0], sum[1]));
+  return s.x + s.y;
+}
+
+// Raw products to scores in log2 units: cap and bias of a row whose first key is at distance d0.
+// tanh x = x Q(x^2) with the polynomial of least relative error (6e-7) for x^2 <= 1, which covers
+// scores up to the cap; a warp that meets a larger one takes tanh's exponential form.
+__device__ __forceinline__ void map_scores(uint32_t (&sr)[kManyKeys], const ScoreMap& map, float slope, float d0,
+                                           bool real) {
+  float big = 0.f;
+  if (map.cap2 > 0.f) {
+#pragma unroll
+    for (int k = 0; k < kManyKeys; k += 2)
+      big = fmaxf(fmaxf(big, fabsf(__uint_as_float(sr[k]))), fabsf(__uint_as_float(sr[k + 1])));
+  }
+  const float unit = map.arg * 0.34657359f;  // x = s * unit (arg is 2 log2(e) of it)
+  const uint64_t slope2 = pack2(slope, slope), scale2 = pack2(map.scale, map.scale), unit2 = pack2(unit, unit);
+  if (map.cap2 > 0.f && __any_sync(0xffffffffu, real && !(big * unit <= 1.f))) {
+#pragma unroll
+    for (int k = 0; k < kManyKeys; ++k)
+      sr[k] = __float_as_uint(fmaf(slope, d0 + static_cast<float>(k), map(__uint_as_float(sr[k]))));
+    return;
+  }
+  const bool capped = map.cap2 > 0.f;
+#pragma unroll
+  for (int k = 0; k < kManyKeys; k += 2) {
+    const uint64_t s = pack2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1]));
+    uint64_t v = mul2(s, scale2);
+    if (capped) {
+      const uint64_t x = mul2(s, unit2), z = mul2(x, x);
+      uint64_t q = fma2(z, pack2(-0.0030670604f, -0.0030670604f), pack2(0.0167431161f, 0.0167431161f));
+      q = fma2(q, z, pack2(-0.0516056754f, -0.0516056754f));
+      q = fma2(q, z, pack2(0.1328143328f, 0.1328143328f));
+      q = fma2(q, z, pack2(-0.3332904279f, -0.3332904279f));
+      q = fma2(q, z, pack2(0.9999994040f, 0.9999994040f));
+      v = mul2(v, q);
+    }
+    const float2 r = unpack2(fma2(pack2(d0 + static_cast<float>(k), d0 + static_cast<float>(k + 1)), slope2, v));
+    sr[k] = __float_as_uint(r.x);
+    sr[k + 1] = __float_as_uint(r.y);
+  }
+}
+
 // A place in a ring of n, and its turn.
 struct Turn {
   int at = 0, ph = 0;
@@ -1029,13 +1120,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         for (int cc = 0; cc < kManyKeys / 32; ++cc)
           tmem_ld_32x32b_x32(ts + 32 * cc, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * cc]));
         tmem_ld_wait();
-        if (mapped) {
-          const float d0 = static_cast<float>(k0 - pos);
-#pragma unroll
-          for (int k = 0; k < kManyKeys; ++k)
-            sr[k] = __float_as_uint(fmaf(slope, d0 + static_cast<float>(k), map(__uint_as_float(sr[k]))));
-        }
-        if (!(k0 >= sure_lo && k0 + kManyKeys - 1 <= sure_hi)) {
+        if (mapped) map_scores(sr, map, slope, static_cast<float>(k0 - pos), real);
+        const bool sure = k0 >= sure_lo && k0 + kManyKeys - 1 <= sure_hi;
+        if (!sure) {
           // visible: lo < k <= hi, or in the prefix (offsets into the tile)
           const int hi = real ? pos - k0 : -1, lo = hdr.window > 0 ? pos - hdr.window - k0 : -1;
           const int pre = real ? p.pre - k0 : 0;
@@ -1045,7 +1132,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         }
         float mx4[4] = {m, -FLT_MAX, -FLT_MAX, -FLT_MAX};
 #pragma unroll
-        for (int k = 0; k < kManyKeys; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], __uint_as_float(sr[k]));
+        for (int k = 0; k < kManyKeys; k += 2)  // (two at once: a three-operand maximum)
+          mx4[(k >> 1) & 3] = fmaxf(fmaxf(mx4[(k >> 1) & 3], __uint_as_float(sr[k])), __uint_as_float(sr[k + 1]));
         float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         // the row keeps its reference maximum until the tile's exceeds it by the slack: weights then
         // stay below 2^kRescaleSlack, and O is rescaled only when some row moves its reference
@@ -1084,20 +1172,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         // P = exp2((s - m) c) in the place of S; no visible key yet: a reference of zero keeps the
         // weights of hidden keys at zero
         const float ref = mx == -FLT_MAX ? 0.f : -mx * c;
-        float rs4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int cc = 0; cc < kManyKeys / 64; ++cc) {
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float p0 = exp2_approx(fmaf(__uint_as_float(sr[64 * cc + 2 * e]), c, ref));
-            const float p1 = exp2_approx(fmaf(__uint_as_float(sr[64 * cc + 2 * e + 1]), c, ref));
-            w[e] = pack_bf16x2(p0, p1);
-            rs4[e & 3] += bf16lo_to_f32(w[e]) + bf16hi_to_f32(w[e]);
-          }
-          tmem_st_32x32b_x32(ts + 32 * cc, w);
-        }
-        l = fmaf(l, corr, (rs4[0] + rs4[1]) + (rs4[2] + rs4[3]));
+        const float rs = sure ? weights<true>(sr, c, ref, ts) : weights<false>(sr, c, ref, ts);
+        l = fmaf(l, corr, rs);
         m = mx;
         tmem_st_wait();
         tc_fence_before();

@@ -815,6 +815,7 @@ ttq_status ttq_qk_norm_rope_paged(const void* qkv_bf16, int64_t seqs, int64_t to
   ttq_status st = check_pool(p, seqs);
   if (st != TTQ_OK) return st;
   if (!std::isfinite(eps) || !(eps > 0.f)) return TTQ_ERR_INVALID_ARG;
+  if (tokens * (heads + 2 * kv_heads) >= (int64_t(1) << 34)) return TTQ_ERR_TOO_LARGE;  // blocks of one grid
   if (!aligned16(qkv_bf16) || !aligned16(q_norm_bf16) || !aligned16(k_norm_bf16) || !aligned16(rope_table) ||
       !aligned16(q_start) || !aligned16(kv_len) || !aligned16(q_out_bf16))
     return TTQ_ERR_MISALIGNED;
@@ -823,8 +824,8 @@ ttq_status ttq_qk_norm_rope_paged(const void* qkv_bf16, int64_t seqs, int64_t to
   if (st != TTQ_OK) return st;
   const ttq::PagedShape s{seqs, tokens, tokens, heads, kv_heads, head_dim};
   return cuda_status(ttq::launch_qk_norm_rope_paged(qkv_bf16, s, q_norm_bf16, k_norm_bf16, eps, rope_table,
-                                                    table_positions, q_start, kv_len, p, q_out_bf16, di->err_word,
-                                                    stream));
+                                                    table_positions, q_start, kv_len, p, q_out_bf16, di->num_sms,
+                                                    di->err_word, stream));
 }
 
 ttq_status ttq_copy_pages(void* k_pool, void* v_pool, int64_t layers, int64_t num_pages, int64_t page_bytes,
@@ -833,6 +834,7 @@ ttq_status ttq_copy_pages(void* k_pool, void* v_pool, int64_t layers, int64_t nu
   if (layers < 1 || layers > 65535 || num_pages < 1 || num_pages > (int64_t(1) << 30) || page_bytes < 16 ||
       page_bytes > (int64_t(1) << 30) || pairs < 1 || pairs > num_pages)
     return TTQ_ERR_INVALID_ARG;
+  if (pairs * ((page_bytes >> 14) + 1) >= (int64_t(1) << 31)) return TTQ_ERR_TOO_LARGE;
   if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(src) || !aligned16(dst) || page_bytes % 16 != 0)
     return TTQ_ERR_MISALIGNED;
   DeviceInfo* di = nullptr;

@@ -278,8 +278,8 @@ cudaError_t launch_paged_attention(const void* q, int64_t ld_q, const PagedShape
                                    cudaStream_t stream);
 cudaError_t launch_qk_norm_rope_paged(const void* qkv, const PagedShape& s, const void* wq, const void* wk, float eps,
                                       const float* rope, int64_t rope_rows, const int32_t* q_start,
-                                      const int32_t* kv_len, const PagePool& p, void* q_out, unsigned* err,
-                                      cudaStream_t stream);
+                                      const int32_t* kv_len, const PagePool& p, void* q_out, int num_sms,
+                                      unsigned* err, cudaStream_t stream);
 cudaError_t launch_copy_pages(void* k, void* v, int64_t layers, int64_t num_pages, int64_t page_bytes,
                               const int32_t* src, const int32_t* dst, int64_t pairs, unsigned* err,
                               cudaStream_t stream);
