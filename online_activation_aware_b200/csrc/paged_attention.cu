@@ -34,7 +34,7 @@ namespace {
 constexpr int kFewRows = 16;       // rows of a tile of few_rows_kernel (one mma.sync block)
 constexpr int kFewKeys = 64;       // its key tile
 constexpr int kHalfRows = 128;     // rows of one tcgen05 block; many_rows_kernel works on two
-constexpr int kManyKeys = 128;     // its key tile
+constexpr int kManyKeys = 64;      // its key tile
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanTiles = 2048;   // tiles whose data the plan keeps in shared memory
 constexpr unsigned kPlanMagic = 0x54545133u;
@@ -741,46 +741,74 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
 
 // ---------------------------------------------------------------- many rows: tcgen05
 
-// 12 warps: 0-3 and 4-7 the softmax of the two halves (128 rows each, a row a thread), 8 copies,
-// 9 products (10 and 11 only complete the warpgroup, whose registers go to the softmax).
-constexpr int kManyThreads = 384;
+// 11 warps: 0-3 and 4-7 the softmax of the two halves (128 rows each, a row a thread), 8 copies, 9
+// and 10 the products of a half each (one warp for both could not issue them fast enough: 2800
+// cycles a key tile, twice what they take). The scores of a half have two places in tensor memory, so that its next product
+// runs while its softmax works. (With one place of twice the keys, a half's softmax and its products
+// took turns: 46% of the tensor cores' cycles, where this form has xx%.)
+constexpr int kManyThreads = 352;
 constexpr float kRescaleSlack = 8.0f;          // log2 units a row maximum may rise before O is rescaled
-constexpr uint32_t kRowBox = kHalfRows * 128;  // 128 rows x 128 B: a box of Q, K or V
+constexpr uint32_t kRowBox = kHalfRows * 128;  // a box of Q: 128 rows x 128 B
+constexpr uint32_t kKeyBox = kManyKeys * 128;  // a box of K or V: 64 rows x 128 B
+constexpr int kManyMaxStages = 10;
 
 struct ManyBars {
-  uint64_t full[8], empty[8];  // the ring of K and V tiles
+  uint64_t full[kManyMaxStages], empty[kManyMaxStages];  // the ring of K and V tiles
   uint64_t q_full, q_empty;
-  uint64_t s_full[2];          // S of a half is in tensor memory
-  uint64_t p_full[2];          // its weights are, in the place of S
-  uint64_t o_full[2];          // O of a half holds the piece's result
+  uint64_t s_full[2][2];       // scores of a half are in a place of tensor memory
+  uint64_t p_full[2][2];       // its weights are, in the same place
+  uint64_t o_done[2];          // a product of a half with V has landed
+  uint64_t o_full[2];          // the last one of a piece has
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
 };
 
-// smem: Q of both halves | ring of tiles K_0 V_0 K_1 V_1 ... (128 positions each), in 1024-byte
-// aligned boxes of 64 channels; barriers. Tensor memory: S of both halves (128 columns each; the
-// weights, two to a column, take the first 64), O of both halves (D columns each).
+// smem: Q of both halves | ring of tiles K_0, K_1 V_0, K_2 V_1, ..., V_last, in 1024-byte aligned
+// boxes of 64 channels; barriers. Tensor memory: the scores of both halves, two places each (64
+// columns; the weights, two to a column, take the first 32), then O of both halves (D columns).
 template <int D>
 struct ManyLayout {
-  static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr uint32_t kTile = (D / 64) * kRowBox;  // Q of a half, or K or V of a key tile
-  static constexpr uint32_t kOffRing = 2 * kTile;
+  static constexpr int kStages = 10;
+  static constexpr uint32_t kQHalf = (D / 64) * kRowBox;
+  static constexpr uint32_t kTile = (D / 64) * kKeyBox;
+  static constexpr uint32_t kOffRing = 2 * kQHalf;
   static constexpr uint32_t kOffBars = kOffRing + kStages * kTile;
   static constexpr size_t kSmem = kOffBars + sizeof(ManyBars) + 1024;
-  static constexpr uint32_t kColS = 0, kColO = 2 * kManyKeys;
+  static constexpr uint32_t kColS = 0, kColO = 4 * kManyKeys;
 };
-static_assert(ManyLayout<128>::kSmem <= 227 * 1024 && ManyLayout<64>::kSmem <= 227 * 1024, "one CTA per SM");
-static_assert(kManyKeys == kHalfRows, "boxes of Q, K and V are alike");
+static_assert(ManyLayout<128>::kSmem <= 227 * 1024, "one CTA per SM");
+static_assert(ManyLayout<128>::kStages <= kManyMaxStages && ManyLayout<64>::kStages <= kManyMaxStages, "");
 
+// Descriptors in two words: the low one holds the address (and the leading byte offset), so that a
+// step along K adds a constant to it.
+struct Desc {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ Desc split(uint64_t d) {
+  return Desc{static_cast<uint32_t>(d), static_cast<uint32_t>(d >> 32)};
+}
+// D[tmem] (+)= A[smem] * B[smem]^T.
+__device__ __forceinline__ void umma_step(uint32_t tmem_d, Desc a, uint32_t a_off, Desc b, uint32_t b_off, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 da, {%1, %2};\n\t"
+      "mov.b64 db, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(tmem_d),
+      "r"(a.lo + (a_off >> 4)), "r"(a.hi), "r"(b.lo + (b_off >> 4)), "r"(b.hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // D[tmem] (+)= A[tmem] * B[smem]: A bf16, a row a lane, two elements a column.
-__device__ __forceinline__ void umma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+__device__ __forceinline__ void umma_step_ta(uint32_t tmem_d, uint32_t tmem_a, Desc b, uint32_t b_off, uint32_t idesc,
                                              uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "r"(b.lo + (b_off >> 4)), "r"(b.hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -814,7 +842,8 @@ __device__ __forceinline__ float weights(uint32_t (&sr)[kManyKeys], float c, flo
     uint32_t w[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
-      uint64_t y2 = fma2(pack2(__uint_as_float(sr[64 * cc + 2 * e]), __uint_as_float(sr[64 * cc + 2 * e + 1])), c2, ref2);
+      const uint64_t y2 =
+          fma2(pack2(__uint_as_float(sr[64 * cc + 2 * e]), __uint_as_float(sr[64 * cc + 2 * e + 1])), c2, ref2);
       float2 y = unpack2(y2);
       if (SURE && (e & 3) == 3) {
         y = exp2_fma2(pack2(fmaxf(y.x, -126.f), fmaxf(y.y, -126.f)));
@@ -896,8 +925,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   const DevErr err = a.err;
   const uint32_t b_full = smem_addr(&bars->full[0]), b_empty = smem_addr(&bars->empty[0]);
   const uint32_t b_q = smem_addr(&bars->q_full), b_qe = smem_addr(&bars->q_empty);
-  const uint32_t b_s = smem_addr(&bars->s_full[0]), b_p = smem_addr(&bars->p_full[0]);
-  const uint32_t b_o = smem_addr(&bars->o_full[0]);
+  const uint32_t b_s = smem_addr(&bars->s_full[0][0]), b_p = smem_addr(&bars->p_full[0][0]);
+  const uint32_t b_o = smem_addr(&bars->o_done[0]), b_of = smem_addr(&bars->o_full[0]);
   const uint32_t b_drain = smem_addr(&bars->drain);
   pdl_enter();  // the plan, q, k and v are written by kernels ahead in the stream
   const PlanHeader hdr = *reinterpret_cast<const PlanHeader*>(a.plan);
@@ -910,16 +939,19 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(b_full + 8 * i, 1);
-      mbar_init(b_empty + 8 * i, 1);
+      mbar_init(b_empty + 8 * i, 2);  // one arrival per half
     }
     mbar_init(b_q, 1);
-    mbar_init(b_qe, 1);
-    for (int i = 0; i < 2; ++i) {
+    mbar_init(b_qe, 2);
+    for (int i = 0; i < 4; ++i) {
       mbar_init(b_s + 8 * i, 1);
       mbar_init(b_p + 8 * i, 4);  // one arrival per softmax warp
-      mbar_init(b_o + 8 * i, 1);
     }
-    mbar_init(b_drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b_o + 8 * i, 1);
+      mbar_init(b_of + 8 * i, 1);
+    }
+    mbar_init(b_drain, 2);
     bars->abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm_q);
@@ -937,167 +969,171 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   const int G = a.G;
   const int tqh = kHalfRows / G;  // tokens of a half
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 8) {
-      // ------------------------------------------------------------ copies
-      Turn t;
-      int issued = 0, q_loads = 0;
-      bool ok = true;
-      for (int pi = range.x; ok && pi < range.y; ++pi) {
-        const Piece p = load_piece(a, pi);
-        if (p.j0 >= p.j1) continue;
-        const Needed nd = needed_keys(p, hdr.window);
-        PageFeed<kManyKeys> feed;
-        feed.start(a, p, nd);
-        // Q: rows are (token, head of the group), a box of G heads x tokens a half; the rows left
-        // over in a half are never stored
-        if (q_loads > 0 && !warp_all(mbar_wait(b_qe, (q_loads - 1) & 1, err, abort_flag))) break;
-        if (lane == 0) {
-          const int halves = p.ntok > tqh ? 2 : 1;
-          mbar_arrive_expect_tx(b_q, halves * (D / 64) * G * tqh * 128);
-          for (int h = 0; h < halves; ++h)
+  if (warp == 8) {
+    // ------------------------------------------------------------ copies
+    Turn t;
+    int issued = 0, q_loads = 0;
+    bool ok = true;
+    for (int pi = range.x; ok && pi < range.y; ++pi) {
+      const Piece p = load_piece(a, pi);
+      if (p.j0 >= p.j1) continue;
+      const Needed nd = needed_keys(p, hdr.window);
+      PageFeed<kManyKeys> feed;
+      feed.start(a, p, nd);
+      // Q: rows are (token, head of the group), a box of G heads x tokens a half; the rows left over
+      // in a half are never stored
+      if (q_loads > 0 && !warp_all(mbar_wait(b_qe, (q_loads - 1) & 1, err, abort_flag))) break;
+      if (lane == 0) {
+        const int halves = p.ntok > tqh ? 2 : 1;
+        mbar_arrive_expect_tx(b_q, halves * (D / 64) * G * tqh * 128);
+        for (int h = 0; h < halves; ++h)
 #pragma unroll
-            for (int bx = 0; bx < D / 64; ++bx)
-              tma_load_3d(base + h * Lay::kTile + bx * kRowBox, &tm_q, b_q, 64 * bx, p.kvh * G, p.tok0 + h * tqh);
+          for (int bx = 0; bx < D / 64; ++bx)
+            tma_load_3d(base + h * Lay::kQHalf + bx * kRowBox, &tm_q, b_q, 64 * bx, p.kvh * G, p.tok0 + h * tqh);
+      }
+      __syncwarp();
+      ++q_loads;
+      const uint32_t off = (lane & ((1 << feed.ppt_log2) - 1)) * (a.page_size * 128);
+      // K or V of the tile whose pages start at row z, by the lanes that hold its pages
+      auto load = [&](const CUtensorMap* map, bool mine, int z) -> bool {
+        if (issued >= S && !warp_all(mbar_wait(b_empty + 8 * t.at, t.ph ^ 1, err, abort_flag))) return false;
+        if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * t.at, Lay::kTile);
+        __syncwarp();
+        if (mine) {
+          const uint32_t to = base + Lay::kOffRing + t.at * Lay::kTile + off;
+#pragma unroll
+          for (int bx = 0; bx < D / 64; ++bx) tma_load_3d(to + bx * kKeyBox, map, b_full + 8 * t.at, 64 * bx, p.kvh, z);
         }
         __syncwarp();
-        ++q_loads;
-        for (int j = p.j0; ok && j < p.j1; ++j) {
-          int z;
-          const bool mine = feed.mine(a, p, j, nd, &z);
-          const uint32_t off = (lane & ((1 << feed.ppt_log2) - 1)) * (a.page_size * 128);
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            if (issued >= S && !warp_all(mbar_wait(b_empty + 8 * t.at, t.ph ^ 1, err, abort_flag))) {
-              ok = false;
-              break;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * t.at, Lay::kTile);
-            __syncwarp();
-            if (mine) {
-              const uint32_t to = base + Lay::kOffRing + t.at * Lay::kTile + off;
-#pragma unroll
-              for (int bx = 0; bx < D / 64; ++bx)
-                tma_load_3d(to + bx * kRowBox, kv ? &tm_v : &tm_k, b_full + 8 * t.at, 64 * bx, p.kvh, z);
-            }
-            __syncwarp();
-            ++issued;
-            t.next(S);
-          }
-        }
-      }
-      if (lane == 0 && *abort_flag) {
-        // every copy this CTA started lands before its shared memory is released
-        if (q_loads > 0) attn_drain(b_q, (q_loads - 1) & 1, err);
-        for (int k = 0; k < min(issued, S); ++k) {
-          if (--t.at < 0) {
-            t.at = S - 1;
-            t.ph ^= 1;
-          }
-          attn_drain(b_full + 8 * t.at, t.ph, err);
-        }
-      }
-    } else if (warp == 9) {
-      // ------------------------------------------------------------ products
-      const uint32_t idesc_s = idesc_bf16_f32(kHalfRows, kManyKeys);
-      const uint32_t idesc_pv = idesc_bf16_f32(kHalfRows, D) | (1u << 16);  // B (V) MN-major
-      Turn t;                       // next tile of the ring to be used
-      int qn = 0, pn[2] = {0, 0};   // uses so far of q_full and p_full
-      bool ok = true;
-      for (int pi = range.x; ok && pi < range.y; ++pi) {
-        const Piece p = load_piece(a, pi);
-        const int nj = p.j1 - p.j0;
-        if (nj <= 0) continue;
-        const int halves = p.ntok > tqh ? 2 : 1;
-        if (!(ok = warp_all(mbar_wait(b_q, qn++ & 1, err, abort_flag)))) break;
-        // S_h = Q_h K^T in the place of S_h (K = D in steps of 16: 4 per 64-channel box)
-        auto issue_s = [&](int h, uint32_t ks) {
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t o = (kk >> 2) * kRowBox + (kk & 3) * 32;
-              umma_bf16(tmem + Lay::kColS + h * kManyKeys, sw128_kmajor_desc(base + h * Lay::kTile + o),
-                        sw128_kmajor_desc(ks + o), idesc_s, kk > 0 ? 1u : 0u);
-            }
-            umma_commit(b_s + 8 * h);
-          }
-          __syncwarp();
-        };
-        auto release = [&](uint32_t bar) {
-          if (elect_one()) umma_commit(bar);
-          __syncwarp();
-        };
-        if (!(ok = warp_all(mbar_wait(b_full + 8 * t.at, t.ph, err, abort_flag)))) break;
-        tc_fence_after();
-        for (int h = 0; h < halves; ++h) issue_s(h, base + Lay::kOffRing + t.at * Lay::kTile);
-        release(b_empty + 8 * t.at);
-        if (nj == 1) release(b_qe);
+        ++issued;
         t.next(S);
-        for (int j = 0; ok && j < nj; ++j) {
-          const Turn tv = t;
+        return true;
+      };
+      bool mine_v = false;
+      int z_v = 0;
+      for (int j = p.j0; ok && j <= p.j1; ++j) {
+        bool mine = false;
+        int z = 0;
+        if (j < p.j1) {
+          mine = feed.mine(a, p, j, nd, &z);
+          ok = load(&tm_k, mine, z);
+        }
+        if (ok && j > p.j0) ok = load(&tm_v, mine_v, z_v);
+        mine_v = mine;
+        z_v = z;
+      }
+    }
+    if (lane == 0 && *abort_flag) {
+      // every copy this CTA started lands before its shared memory is released
+      if (q_loads > 0) attn_drain(b_q, (q_loads - 1) & 1, err);
+      for (int k = 0; k < min(issued, S); ++k) {
+        if (--t.at < 0) {
+          t.at = S - 1;
+          t.ph ^= 1;
+        }
+        attn_drain(b_full + 8 * t.at, t.ph, err);
+      }
+    }
+  } else if (warp >= 9) {
+    // ------------------------------------------------------------ products of a half
+    const int h = warp - 9;
+    constexpr uint32_t idesc_s = idesc_bf16_f32(kHalfRows, kManyKeys);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(kHalfRows, D) | (1u << 16);  // B (V) MN-major
+    const Desc qd = split(sw128_kmajor_desc(base + h * Lay::kQHalf));
+    const Desc kd = split(sw128_kmajor_desc(base + Lay::kOffRing));
+    const Desc vd = split(sw128_mnmajor_desc(base + Lay::kOffRing, kKeyBox));
+    const uint32_t o_col = tmem + Lay::kColO + h * D;
+    Turn t;                 // next tile of the ring to be used
+    int qn = 0;             // uses so far of q_full
+    uint32_t pn = 0;        // bit `place`: turn of p_full
+    bool ok = true;
+    for (int pi = range.x; ok && pi < range.y; ++pi) {
+      const Piece p = load_piece(a, pi);
+      const int nj = p.j1 - p.j0;
+      if (nj <= 0) continue;
+      // a half without rows only lets the ring go on
+      const bool rows = h == 0 || p.ntok > tqh;
+      auto release = [&](uint32_t bar) {
+        if (elect_one()) {
+          if (rows) umma_commit(bar);
+          else mbar_arrive(bar);
+        }
+        __syncwarp();
+      };
+      if (!(ok = warp_all(mbar_wait(b_q, qn++ & 1, err, abort_flag)))) break;
+      for (int i = 0; i <= nj; ++i) {
+        if (i < nj) {
+          // S = Q K_i^T into place i & 1 (K = D in steps of 16: 4 per 64-channel box); the weights that
+          // were there have been multiplied by an earlier product of this warp
+          if (!(ok = warp_all(mbar_wait(b_full + 8 * t.at, t.ph, err, abort_flag)))) break;
+          tc_fence_after();
+          const uint32_t tile = t.at * Lay::kTile, place = 2 * h + (i & 1);
+          if (rows && elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_step(tmem + Lay::kColS + place * kManyKeys, qd, (kk >> 2) * kRowBox + (kk & 3) * 32, kd,
+                        tile + (kk >> 2) * kKeyBox + (kk & 3) * 32, idesc_s, kk > 0 ? 1u : 0u);
+            umma_commit(b_s + 8 * place);
+          }
+          __syncwarp();
+          release(b_empty + 8 * t.at);
+          if (i == nj - 1) release(b_qe);
           t.next(S);
-          const Turn tk = t;
-          if (j + 1 < nj) t.next(S);
-          if (!(ok = warp_all(mbar_wait(b_full + 8 * tv.at, tv.ph, err, abort_flag)))) break;
-          for (int h = 0; h < halves; ++h) {
-            // (weights of a piece's first tile come after O_h of the piece before has been read)
-            if (!(ok = warp_all(mbar_wait(b_p + 8 * h, pn[h]++ & 1, err, abort_flag)))) break;
+        }
+        if (i > 0) {
+          // O += P V_{i-1}: K = 64 positions in steps of 16 (8 columns of P; two 8-row groups of V, the
+          // next 64 channels one box on). The weights of a piece's first tile come after the last piece's
+          // O has been read.
+          const uint32_t tile = t.at * Lay::kTile, place = 2 * h + ((i - 1) & 1);
+          if (!(ok = warp_all(mbar_wait(b_full + 8 * t.at, t.ph, err, abort_flag)))) break;
+          if (rows) {
+            if (!(ok = warp_all(mbar_wait(b_p + 8 * place, pn >> place & 1, err, abort_flag)))) break;
+            pn ^= 1u << place;
             tc_fence_after();
             if (elect_one()) {
-              // O_h += P_h V: K = 128 positions in steps of 16 (8 columns of P; two 8-row groups of V,
-              // the next 64 channels one box on)
-              const uint32_t vs = base + Lay::kOffRing + tv.at * Lay::kTile;
 #pragma unroll
               for (int kk = 0; kk < kManyKeys / 16; ++kk)
-                umma_bf16_ta(tmem + Lay::kColO + h * D, tmem + Lay::kColS + h * kManyKeys + kk * 8,
-                             sw128_mnmajor_desc(vs + kk * 2048, kRowBox), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+                umma_step_ta(o_col, tmem + Lay::kColS + place * kManyKeys + kk * 8, vd, tile + kk * 2048, idesc_pv,
+                             (i > 1 || kk > 0) ? 1u : 0u);
+              umma_commit(b_o + 8 * h);
+              if (i == nj) umma_commit(b_of + 8 * h);
             }
             __syncwarp();
-            if (h == halves - 1) release(b_empty + 8 * tv.at);
-            if (j + 1 < nj) {
-              if (h == 0) {
-                if (!(ok = warp_all(mbar_wait(b_full + 8 * tk.at, tk.ph, err, abort_flag)))) break;
-                tc_fence_after();
-              }
-              issue_s(h, base + Lay::kOffRing + tk.at * Lay::kTile);
-              if (h == halves - 1) {
-                release(b_empty + 8 * tk.at);
-                if (j + 2 == nj) release(b_qe);
-              }
-            } else {
-              release(b_o + 8 * h);
-            }
           }
+          release(b_empty + 8 * t.at);
+          t.next(S);
         }
       }
-      // every product issued above completes before tensor memory is released
-      if (elect_one()) umma_commit(b_drain);
-      __syncwarp();
-      attn_drain(b_drain, 0, err);
     }
+    // every product issued above completes before tensor memory is released
+    if (elect_one()) umma_commit(b_drain);
+    __syncwarp();
+    attn_drain(b_drain, 0, err);
   } else {
     // ------------------------------------------------------------ softmax, a row a thread
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int h = warp >> 2;
     const int quad = warp & 3;
     const int r = quad * 32 + lane;
-    const uint32_t ts = tmem + (static_cast<uint32_t>(quad * 32) << 16) + Lay::kColS + h * kManyKeys;
-    const uint32_t to = tmem + (static_cast<uint32_t>(quad * 32) << 16) + Lay::kColO + h * D;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t to = lanes + Lay::kColO + h * D;
     const ScoreMap map = score_map(a);
     const bool mapped = a.cap > 0.f || a.slopes != nullptr;
     // scores enter the exponent as s * c (raw products), or as they are once mapped
     const float c = mapped ? 1.f : a.scale_log2;
     const float slack = kRescaleSlack / c;
     const int rt = r / G, rg = r % G;
-    Turn tv;        // the ring's place of this key tile's V (looked at by the first half alone)
-    int sn = 0, on = 0;  // uses so far of s_full and o_full
+    int tiles = 0;           // of the ring, before this piece
+    uint32_t sn = 0;         // bit `place`: turn of s_full
+    int dn = 0, on = 0;      // products so far: of any tile, of a piece's last
     bool ok = true;
     for (int pi = range.x; ok && pi < range.y; ++pi) {
       const Piece p = load_piece(a, pi);
       const int nj = p.j1 - p.j0;
       const int tok = h * tqh + rt;
-      if (h == 1 && p.ntok <= tqh) continue;
+      if (h == 1 && p.ntok <= tqh) {
+        tiles += 2 * nj;
+        continue;
+      }
       const Needed nd = needed_keys(p, hdr.window);
       const bool real = rt < tqh && tok < p.ntok;
       const int head = p.kvh * G + rg;
@@ -1109,11 +1145,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       float m = -FLT_MAX, l = 0.f;
       for (int j = 0; j < nj; ++j) {
         const int k0 = key_tile(p, p.j0 + j) * kManyKeys;
-        tv.next(S);  // past K
-        if (!warp_all(mbar_wait(b_s + 8 * h, sn++ & 1, err, abort_flag))) {
+        const int place = 2 * h + (j & 1);
+        const uint32_t ts = lanes + Lay::kColS + place * kManyKeys;
+        if (!warp_all(mbar_wait(b_s + 8 * place, sn >> (j & 1) & 1, err, abort_flag))) {
           ok = false;
           break;
         }
+        sn ^= 1u << (j & 1);
         tc_fence_after();
         uint32_t sr[kManyKeys];
 #pragma unroll
@@ -1137,51 +1175,60 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         // the row keeps its reference maximum until the tile's exceeds it by the slack: weights then
         // stay below 2^kRescaleSlack, and O is rescaled only when some row moves its reference
-        if (mx <= m + slack) mx = m;
-        const float corr = real ? exp2_approx((m - mx) * c) : 1.f;  // (rows that are not there hold anything)
-        // (S_j complete means P_{j-1} V_{j-1} complete: the products of a half run in order)
-        if (j > 0 && __any_sync(0xffffffffu, corr != 1.f ? 1 : 0)) {
+        if (mx <= m + slack || !real) mx = m;  // (rows that are not there hold anything)
+        if (__any_sync(0xffffffffu, mx != m ? 1 : 0)) {
+          const float corr = exp2_approx((m - mx) * c);
+          if (j > 0) {
+            // P_{j-1} V_{j-1} has landed (P_{j-2} V_{j-2} has: S_j came after it)
+            if (!warp_all(mbar_wait(b_o + 8 * h, (dn - 1) & 1, err, abort_flag))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
 #pragma unroll 1
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(to + 32 * cc, o);
-            tmem_ld_wait();
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(to + 32 * cc, o);
+              tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__fmul_rn(__uint_as_float(o[e]), corr));
-            tmem_st_32x32b_x32(to + 32 * cc, o);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__fmul_rn(__uint_as_float(o[e]), corr));
+              tmem_st_32x32b_x32(to + 32 * cc, o);
+            }
           }
+          l *= corr;
+          m = mx;
         }
-        if (h == 0 && !nd.all(k0, k0 + kManyKeys)) {
+        if (!nd.all(k0, k0 + kManyKeys)) {
           // rows of V that no token sees may hold anything: their weight is zero, so make them zero
-          // (the products of both halves wait for the first half's weights)
-          if (!warp_all(mbar_wait(b_full + 8 * tv.at, tv.ph, err, abort_flag))) {
+          // (both halves do, each ahead of its own product)
+          const int at = tiles + (j + 1 < nj ? 2 * j + 2 : 2 * nj - 1);
+          if (!warp_all(mbar_wait(b_full + 8 * (at % S), at / S & 1, err, abort_flag))) {
             ok = false;
             break;
           }
-          if (!nd.at(k0 + r)) {
-            const uint32_t vr = base + Lay::kOffRing + tv.at * Lay::kTile + r * 128;
+          if (!nd.at(k0 + (r >> 1))) {
+            const uint32_t vr = base + Lay::kOffRing + (at % S) * Lay::kTile + (r >> 1) * 128 + (r & 1) * 64;
 #pragma unroll
             for (int bx = 0; bx < D / 64; ++bx)
 #pragma unroll
-              for (int q = 0; q < 8; ++q)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vr + bx * kRowBox + q * 16), "r"(0)
+              for (int q = 0; q < 4; ++q)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vr + bx * kKeyBox + q * 16), "r"(0)
                              : "memory");
           }
           fence_proxy_async_smem();
         }
         // P = exp2((s - m) c) in the place of S; no visible key yet: a reference of zero keeps the
         // weights of hidden keys at zero
-        const float ref = mx == -FLT_MAX ? 0.f : -mx * c;
-        const float rs = sure ? weights<true>(sr, c, ref, ts) : weights<false>(sr, c, ref, ts);
-        l = fmaf(l, corr, rs);
-        m = mx;
+        const float ref = m == -FLT_MAX ? 0.f : -m * c;
+        l += sure ? weights<true>(sr, c, ref, ts) : weights<false>(sr, c, ref, ts);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b_p + 8 * h);
-        tv.next(S);  // past V
+        if (lane == 0) mbar_arrive(b_p + 8 * place);
+        ++dn;
       }
-      if (!ok || (nj > 0 && !warp_all(mbar_wait(b_o + 8 * h, on++ & 1, err, abort_flag)))) {
+      tiles += 2 * nj;
+      if (!ok || (nj > 0 && !warp_all(mbar_wait(b_of + 8 * h, on++ & 1, err, abort_flag)))) {
         ok = false;
         break;
       }
@@ -1215,7 +1262,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           for (int q4 = 0; q4 < 8; ++q4)
             *reinterpret_cast<uint4*>(a.acc + prow * D + 32 * cc + 4 * q4) =
                 make_uint4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
-          if (cc == 0) a.ml[prow] = make_float2(mapped ? m : m * c, l);
+          if (cc == 0) a.ml[prow] = make_float2(m * c, l);
         }
       }
     }
