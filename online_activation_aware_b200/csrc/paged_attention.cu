@@ -750,10 +750,10 @@ constexpr int kManyThreads = 352;
 constexpr float kRescaleSlack = 8.0f;          // log2 units a row maximum may rise before O is rescaled
 constexpr uint32_t kRowBox = kHalfRows * 128;  // a box of Q: 128 rows x 128 B
 constexpr uint32_t kKeyBox = kManyKeys * 128;  // a box of K or V: 64 rows x 128 B
-constexpr int kManyMaxStages = 10;
+constexpr int kManyMaxStages = 8;
 
 struct ManyBars {
-  uint64_t full[kManyMaxStages], empty[kManyMaxStages];  // the ring of K and V tiles
+  uint64_t full[kManyMaxStages], empty[kManyMaxStages];  // the ring of K and V
   uint64_t q_full, q_empty;
   uint64_t s_full[2][2];       // scores of a half are in a place of tensor memory
   uint64_t p_full[2][2];       // its weights are, in the same place
@@ -764,16 +764,17 @@ struct ManyBars {
   int abort_flag;
 };
 
-// smem: Q of both halves | ring of tiles K_0, K_1 V_0, K_2 V_1, ..., V_last, in 1024-byte aligned
-// boxes of 64 channels; barriers. Tensor memory: the scores of both halves, two places each (64
+// smem: Q of both halves | ring of stages (K_i, V_{i-1}), in 1024-byte aligned boxes of 64 channels;
+// barriers. Tensor memory: the scores of both halves, two places each (64
 // columns; the weights, two to a column, take the first 32), then O of both halves (D columns).
 template <int D>
 struct ManyLayout {
-  static constexpr int kStages = 10;
+  static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr uint32_t kQHalf = (D / 64) * kRowBox;
   static constexpr uint32_t kTile = (D / 64) * kKeyBox;
   static constexpr uint32_t kOffRing = 2 * kQHalf;
-  static constexpr uint32_t kOffBars = kOffRing + kStages * kTile;
+  static constexpr uint32_t kStage = 2 * kTile;  // K, then V
+  static constexpr uint32_t kOffBars = kOffRing + kStages * kStage;
   static constexpr size_t kSmem = kOffBars + sizeof(ManyBars) + 1024;
   static constexpr uint32_t kColS = 0, kColO = 4 * kManyKeys;
 };
@@ -899,6 +900,13 @@ __device__ __forceinline__ void map_scores(uint32_t (&sr)[kManyKeys], const Scor
   }
 }
 
+// A wait of the whole warp: one lane asks, all learn.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const DevErr& err, volatile int* abort_flag) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, err, abort_flag);
+  return warp_all(ok);
+}
+
 // A place in a ring of n, and its turn.
 struct Turn {
   int at = 0, ph = 0;
@@ -994,33 +1002,32 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       __syncwarp();
       ++q_loads;
       const uint32_t off = (lane & ((1 << feed.ppt_log2) - 1)) * (a.page_size * 128);
-      // K or V of the tile whose pages start at row z, by the lanes that hold its pages
-      auto load = [&](const CUtensorMap* map, bool mine, int z) -> bool {
-        if (issued >= S && !warp_all(mbar_wait(b_empty + 8 * t.at, t.ph ^ 1, err, abort_flag))) return false;
-        if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * t.at, Lay::kTile);
-        __syncwarp();
-        if (mine) {
-          const uint32_t to = base + Lay::kOffRing + t.at * Lay::kTile + off;
-#pragma unroll
-          for (int bx = 0; bx < D / 64; ++bx) tma_load_3d(to + bx * kKeyBox, map, b_full + 8 * t.at, 64 * bx, p.kvh, z);
-        }
-        __syncwarp();
-        ++issued;
-        t.next(S);
-        return true;
-      };
       bool mine_v = false;
       int z_v = 0;
-      for (int j = p.j0; ok && j <= p.j1; ++j) {
+      for (int j = p.j0; j <= p.j1; ++j) {
+        // K of tile j and V of the one before it, by the lanes that hold their pages
         bool mine = false;
         int z = 0;
-        if (j < p.j1) {
-          mine = feed.mine(a, p, j, nd, &z);
-          ok = load(&tm_k, mine, z);
+        if (j < p.j1) mine = feed.mine(a, p, j, nd, &z);
+        if (issued >= S && !(ok = warp_all(mbar_wait(b_empty + 8 * t.at, t.ph ^ 1, err, abort_flag)))) break;
+        if (lane == 0)
+          mbar_arrive_expect_tx(b_full + 8 * t.at, (j < p.j1 && j > p.j0 ? 2 : 1) * Lay::kTile);
+        __syncwarp();
+        const uint32_t to = base + Lay::kOffRing + t.at * Lay::kStage + off;
+        if (mine) {
+#pragma unroll
+          for (int bx = 0; bx < D / 64; ++bx) tma_load_3d(to + bx * kKeyBox, &tm_k, b_full + 8 * t.at, 64 * bx, p.kvh, z);
         }
-        if (ok && j > p.j0) ok = load(&tm_v, mine_v, z_v);
+        if (mine_v) {
+#pragma unroll
+          for (int bx = 0; bx < D / 64; ++bx)
+            tma_load_3d(to + Lay::kTile + bx * kKeyBox, &tm_v, b_full + 8 * t.at, 64 * bx, p.kvh, z_v);
+        }
+        __syncwarp();
         mine_v = mine;
         z_v = z;
+        ++issued;
+        t.next(S);
       }
     }
     if (lane == 0 && *abort_flag) {
@@ -1041,7 +1048,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     constexpr uint32_t idesc_pv = idesc_bf16_f32(kHalfRows, D) | (1u << 16);  // B (V) MN-major
     const Desc qd = split(sw128_kmajor_desc(base + h * Lay::kQHalf));
     const Desc kd = split(sw128_kmajor_desc(base + Lay::kOffRing));
-    const Desc vd = split(sw128_mnmajor_desc(base + Lay::kOffRing, kKeyBox));
+    const Desc vd = split(sw128_mnmajor_desc(base + Lay::kOffRing + Lay::kTile, kKeyBox));
     const uint32_t o_col = tmem + Lay::kColO + h * D;
     Turn t;                 // next tile of the ring to be used
     int qn = 0;             // uses so far of q_full
@@ -1060,49 +1067,45 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         }
         __syncwarp();
       };
-      if (!(ok = warp_all(mbar_wait(b_q, qn++ & 1, err, abort_flag)))) break;
+      if (!(ok = warp_wait(b_q, qn++ & 1, err, abort_flag))) break;
       for (int i = 0; i <= nj; ++i) {
-        if (i < nj) {
+        if (!(ok = warp_wait(b_full + 8 * t.at, t.ph, err, abort_flag))) break;
+        tc_fence_after();
+        const uint32_t stage = t.at * Lay::kStage;
+        if (rows && i < nj) {
           // S = Q K_i^T into place i & 1 (K = D in steps of 16: 4 per 64-channel box); the weights that
           // were there have been multiplied by an earlier product of this warp
-          if (!(ok = warp_all(mbar_wait(b_full + 8 * t.at, t.ph, err, abort_flag)))) break;
-          tc_fence_after();
-          const uint32_t tile = t.at * Lay::kTile, place = 2 * h + (i & 1);
-          if (rows && elect_one()) {
+          const uint32_t place = 2 * h + (i & 1);
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               umma_step(tmem + Lay::kColS + place * kManyKeys, qd, (kk >> 2) * kRowBox + (kk & 3) * 32, kd,
-                        tile + (kk >> 2) * kKeyBox + (kk & 3) * 32, idesc_s, kk > 0 ? 1u : 0u);
+                        stage + (kk >> 2) * kKeyBox + (kk & 3) * 32, idesc_s, kk > 0 ? 1u : 0u);
             umma_commit(b_s + 8 * place);
           }
           __syncwarp();
-          release(b_empty + 8 * t.at);
-          if (i == nj - 1) release(b_qe);
-          t.next(S);
         }
-        if (i > 0) {
+        if (i == nj - 1) release(b_qe);
+        if (rows && i > 0) {
           // O += P V_{i-1}: K = 64 positions in steps of 16 (8 columns of P; two 8-row groups of V, the
           // next 64 channels one box on). The weights of a piece's first tile come after the last piece's
           // O has been read.
-          const uint32_t tile = t.at * Lay::kTile, place = 2 * h + ((i - 1) & 1);
-          if (!(ok = warp_all(mbar_wait(b_full + 8 * t.at, t.ph, err, abort_flag)))) break;
-          if (rows) {
-            if (!(ok = warp_all(mbar_wait(b_p + 8 * place, pn >> place & 1, err, abort_flag)))) break;
-            pn ^= 1u << place;
-            tc_fence_after();
-            if (elect_one()) {
+          const uint32_t place = 2 * h + ((i - 1) & 1);
+          if (!(ok = warp_wait(b_p + 8 * place, pn >> place & 1, err, abort_flag))) break;
+          pn ^= 1u << place;
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < kManyKeys / 16; ++kk)
-                umma_step_ta(o_col, tmem + Lay::kColS + place * kManyKeys + kk * 8, vd, tile + kk * 2048, idesc_pv,
-                             (i > 1 || kk > 0) ? 1u : 0u);
-              umma_commit(b_o + 8 * h);
-              if (i == nj) umma_commit(b_of + 8 * h);
-            }
-            __syncwarp();
+            for (int kk = 0; kk < kManyKeys / 16; ++kk)
+              umma_step_ta(o_col, tmem + Lay::kColS + place * kManyKeys + kk * 8, vd, stage + kk * 2048, idesc_pv,
+                           (i > 1 || kk > 0) ? 1u : 0u);
+            umma_commit(b_o + 8 * h);
+            if (i == nj) umma_commit(b_of + 8 * h);
           }
-          release(b_empty + 8 * t.at);
-          t.next(S);
+          __syncwarp();
         }
+        release(b_empty + 8 * t.at);
+        t.next(S);
       }
     }
     // every product issued above completes before tensor memory is released
@@ -1122,7 +1125,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const float c = mapped ? 1.f : a.scale_log2;
     const float slack = kRescaleSlack / c;
     const int rt = r / G, rg = r % G;
-    int tiles = 0;           // of the ring, before this piece
+    int stages = 0;          // of the ring, before this piece
     uint32_t sn = 0;         // bit `place`: turn of s_full
     int dn = 0, on = 0;      // products so far: of any tile, of a piece's last
     bool ok = true;
@@ -1131,7 +1134,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const int nj = p.j1 - p.j0;
       const int tok = h * tqh + rt;
       if (h == 1 && p.ntok <= tqh) {
-        tiles += 2 * nj;
+        stages += nj > 0 ? nj + 1 : 0;
         continue;
       }
       const Needed nd = needed_keys(p, hdr.window);
@@ -1201,13 +1204,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (!nd.all(k0, k0 + kManyKeys)) {
           // rows of V that no token sees may hold anything: their weight is zero, so make them zero
           // (both halves do, each ahead of its own product)
-          const int at = tiles + (j + 1 < nj ? 2 * j + 2 : 2 * nj - 1);
+          const int at = stages + j + 1;
           if (!warp_all(mbar_wait(b_full + 8 * (at % S), at / S & 1, err, abort_flag))) {
             ok = false;
             break;
           }
           if (!nd.at(k0 + (r >> 1))) {
-            const uint32_t vr = base + Lay::kOffRing + (at % S) * Lay::kTile + (r >> 1) * 128 + (r & 1) * 64;
+            const uint32_t vr =
+                base + Lay::kOffRing + (at % S) * Lay::kStage + Lay::kTile + (r >> 1) * 128 + (r & 1) * 64;
 #pragma unroll
             for (int bx = 0; bx < D / 64; ++bx)
 #pragma unroll
@@ -1227,7 +1231,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (lane == 0) mbar_arrive(b_p + 8 * place);
         ++dn;
       }
-      tiles += 2 * nj;
+      stages += nj > 0 ? nj + 1 : 0;
       if (!ok || (nj > 0 && !warp_all(mbar_wait(b_of + 8 * h, on++ & 1, err, abort_flag)))) {
         ok = false;
         break;
