@@ -35,7 +35,7 @@ constexpr int kFewRows = 16;       // rows of a tile of few_rows_kernel (one mma
 constexpr int kFewKeys = 64;       // its key tile
 constexpr int kHalfRows = 128;     // rows of one tcgen05 block; many_rows_kernel works on two
 constexpr int kManyKeys = 64;      // its key tile
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;   // (1024 took twice as long: the idle ones run the scans too)
 constexpr int kPlanTiles = 2048;   // tiles whose data the plan keeps in shared memory
 constexpr unsigned kPlanMagic = 0x54545133u;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -152,16 +152,16 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* total, uint
   const uint64_t x = warp_scan(v);
   if (lane == 31) sh[turn][warp] = x;
   __syncthreads();
-  const uint64_t w = warp_scan(sh[turn][lane]);
+  const uint64_t w = warp_scan(lane < kPlanThreads / 32 ? sh[turn][lane] : 0);
   turn ^= 1;
   *total = __shfl_sync(0xffffffffu, w, 31);
   const uint64_t before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
   return (warp > 0 ? before : 0) + x - v;
 }
 
-// floor(a / d) with inv = 1 / d (exact: the estimate is off by one at most).
-__device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t d, double inv) {
-  uint64_t q = static_cast<uint64_t>(static_cast<double>(a) * inv);
+// floor(a / d), at most the number of blocks, with inv about 1 / d (the estimate is off by one at most).
+__device__ __forceinline__ uint32_t divide(uint64_t a, uint64_t d, float inv) {
+  uint32_t q = static_cast<uint32_t>(static_cast<float>(a) * inv);
   if (q * d > a) --q;
   if ((q + 1) * d <= a) ++q;
   return q;
@@ -207,7 +207,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
     const int n = b < h.seqs ? q_start[b + 1] - q_start[b] : 0;
     uint64_t tot;
     const int at = static_cast<int>(sum + block_scan((n + l.tq - 1) / l.tq, &tot, sh, turn));
-    for (int i = 0; i * l.tq < n; ++i) tile_seq[at + i] = make_int2(b, i * l.tq);
+    // a long sequence's tiles are written by its whole warp
+    const int nt = (n + l.tq - 1) / l.tq;
+    unsigned wide = __ballot_sync(0xffffffffu, nt > 4);
+    if (nt <= 4)
+      for (int i = 0; i < nt; ++i) tile_seq[at + i] = make_int2(b, i * l.tq);
+    while (wide) {
+      const int src = __ffs(wide) - 1;
+      wide &= wide - 1;
+      const int b1 = __shfl_sync(0xffffffffu, b, src), at1 = __shfl_sync(0xffffffffu, at, src);
+      const int nt1 = __shfl_sync(0xffffffffu, nt, src);
+      for (int i = tid & 31; i < nt1; i += 32) tile_seq[at1 + i] = make_int2(b1, i * l.tq);
+    }
     sum += tot;
   }
   const int ntiles = static_cast<int>(sum);
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
   __syncthreads();
   // equal shares; a share shorter than a few key tiles is not worth its start
   const uint64_t share = max(static_cast<uint64_t>(4), (work + l.ctas - 1) / l.ctas);
-  const double inv_share = 1.0 / static_cast<double>(share);
+  const float inv_share = 1.f / static_cast<float>(share);
   // pieces of every item (tile, kv head), scanned as (pieces, slots, splits) in 32 + 16 + 16 bits
   const int items = ntiles * h.kv_heads;
   uint64_t base = 0;
@@ -249,7 +260,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
     const int i = i0 + tid;
     Piece p = {};
     TileKeys k = {};
-    uint64_t a = 0, v = 0, tot, c0 = 0;
+    uint64_t a = 0, v = 0, tot;
+    uint32_t c0 = 0;
     int np = 0, cost = 1;
     if (i < items) {
       const int t = i / h.kv_heads;
@@ -258,7 +270,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
       cost = tile_cost(k.total);
       a = tile_at[t] + static_cast<uint64_t>(p.kvh) * cost;
       c0 = divide(a, share, inv_share);
-      np = static_cast<int>(divide(a + cost - 1, share, inv_share) - c0) + 1;
+      np = static_cast<int>(divide(a + cost - 1, share, inv_share) - c0 + 1);
       v = static_cast<uint64_t>(np) << 32 | (np > 1 ? static_cast<uint64_t>(np) << 16 | 1u : 0u);
     }
     const uint64_t here = base + block_scan(v, &tot, sh, turn);
@@ -750,10 +762,10 @@ constexpr int kManyThreads = 352;
 constexpr float kRescaleSlack = 8.0f;          // log2 units a row maximum may rise before O is rescaled
 constexpr uint32_t kRowBox = kHalfRows * 128;  // a box of Q: 128 rows x 128 B
 constexpr uint32_t kKeyBox = kManyKeys * 128;  // a box of K or V: 64 rows x 128 B
-constexpr int kManyMaxStages = 8;
+constexpr int kManyMaxStages = 10;
 
 struct ManyBars {
-  uint64_t full[kManyMaxStages], empty[kManyMaxStages];  // the ring of K and V
+  uint64_t full[kManyMaxStages], empty[kManyMaxStages];  // the ring of K and V tiles
   uint64_t q_full, q_empty;
   uint64_t s_full[2][2];       // scores of a half are in a place of tensor memory
   uint64_t p_full[2][2];       // its weights are, in the same place
@@ -764,17 +776,16 @@ struct ManyBars {
   int abort_flag;
 };
 
-// smem: Q of both halves | ring of stages (K_i, V_{i-1}), in 1024-byte aligned boxes of 64 channels;
-// barriers. Tensor memory: the scores of both halves, two places each (64
+// smem: Q of both halves | ring of tiles K_0, K_1 V_0, K_2 V_1, ..., V_last, in 1024-byte aligned
+// boxes of 64 channels; barriers. Tensor memory: the scores of both halves, two places each (64
 // columns; the weights, two to a column, take the first 32), then O of both halves (D columns).
 template <int D>
 struct ManyLayout {
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = 10;
   static constexpr uint32_t kQHalf = (D / 64) * kRowBox;
   static constexpr uint32_t kTile = (D / 64) * kKeyBox;
   static constexpr uint32_t kOffRing = 2 * kQHalf;
-  static constexpr uint32_t kStage = 2 * kTile;  // K, then V
-  static constexpr uint32_t kOffBars = kOffRing + kStages * kStage;
+  static constexpr uint32_t kOffBars = kOffRing + kStages * kTile;
   static constexpr size_t kSmem = kOffBars + sizeof(ManyBars) + 1024;
   static constexpr uint32_t kColS = 0, kColO = 4 * kManyKeys;
 };
@@ -900,13 +911,6 @@ __device__ __forceinline__ void map_scores(uint32_t (&sr)[kManyKeys], const Scor
   }
 }
 
-// A wait of the whole warp: one lane asks, all learn.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const DevErr& err, volatile int* abort_flag) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, err, abort_flag);
-  return warp_all(ok);
-}
-
 // A place in a ring of n, and its turn.
 struct Turn {
   int at = 0, ph = 0;
@@ -1002,32 +1006,33 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       __syncwarp();
       ++q_loads;
       const uint32_t off = (lane & ((1 << feed.ppt_log2) - 1)) * (a.page_size * 128);
-      bool mine_v = false;
-      int z_v = 0;
-      for (int j = p.j0; j <= p.j1; ++j) {
-        // K of tile j and V of the one before it, by the lanes that hold their pages
-        bool mine = false;
-        int z = 0;
-        if (j < p.j1) mine = feed.mine(a, p, j, nd, &z);
-        if (issued >= S && !(ok = warp_all(mbar_wait(b_empty + 8 * t.at, t.ph ^ 1, err, abort_flag)))) break;
-        if (lane == 0)
-          mbar_arrive_expect_tx(b_full + 8 * t.at, (j < p.j1 && j > p.j0 ? 2 : 1) * Lay::kTile);
+      // K or V of the tile whose pages start at row z, by the lanes that hold its pages
+      auto load = [&](const CUtensorMap* map, bool mine, int z) -> bool {
+        if (issued >= S && !warp_all(mbar_wait(b_empty + 8 * t.at, t.ph ^ 1, err, abort_flag))) return false;
+        if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * t.at, Lay::kTile);
         __syncwarp();
-        const uint32_t to = base + Lay::kOffRing + t.at * Lay::kStage + off;
         if (mine) {
+          const uint32_t to = base + Lay::kOffRing + t.at * Lay::kTile + off;
 #pragma unroll
-          for (int bx = 0; bx < D / 64; ++bx) tma_load_3d(to + bx * kKeyBox, &tm_k, b_full + 8 * t.at, 64 * bx, p.kvh, z);
-        }
-        if (mine_v) {
-#pragma unroll
-          for (int bx = 0; bx < D / 64; ++bx)
-            tma_load_3d(to + Lay::kTile + bx * kKeyBox, &tm_v, b_full + 8 * t.at, 64 * bx, p.kvh, z_v);
+          for (int bx = 0; bx < D / 64; ++bx) tma_load_3d(to + bx * kKeyBox, map, b_full + 8 * t.at, 64 * bx, p.kvh, z);
         }
         __syncwarp();
-        mine_v = mine;
-        z_v = z;
         ++issued;
         t.next(S);
+        return true;
+      };
+      bool mine_v = false;
+      int z_v = 0;
+      for (int j = p.j0; ok && j <= p.j1; ++j) {
+        bool mine = false;
+        int z = 0;
+        if (j < p.j1) {
+          mine = feed.mine(a, p, j, nd, &z);
+          ok = load(&tm_k, mine, z);
+        }
+        if (ok && j > p.j0) ok = load(&tm_v, mine_v, z_v);
+        mine_v = mine;
+        z_v = z;
       }
     }
     if (lane == 0 && *abort_flag) {
@@ -1048,7 +1053,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     constexpr uint32_t idesc_pv = idesc_bf16_f32(kHalfRows, D) | (1u << 16);  // B (V) MN-major
     const Desc qd = split(sw128_kmajor_desc(base + h * Lay::kQHalf));
     const Desc kd = split(sw128_kmajor_desc(base + Lay::kOffRing));
-    const Desc vd = split(sw128_mnmajor_desc(base + Lay::kOffRing + Lay::kTile, kKeyBox));
+    const Desc vd = split(sw128_mnmajor_desc(base + Lay::kOffRing, kKeyBox));
     const uint32_t o_col = tmem + Lay::kColO + h * D;
     Turn t;                 // next tile of the ring to be used
     int qn = 0;             // uses so far of q_full
@@ -1067,45 +1072,49 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         }
         __syncwarp();
       };
-      if (!(ok = warp_wait(b_q, qn++ & 1, err, abort_flag))) break;
+      if (!(ok = warp_all(mbar_wait(b_q, qn++ & 1, err, abort_flag)))) break;
       for (int i = 0; i <= nj; ++i) {
-        if (!(ok = warp_wait(b_full + 8 * t.at, t.ph, err, abort_flag))) break;
-        tc_fence_after();
-        const uint32_t stage = t.at * Lay::kStage;
-        if (rows && i < nj) {
+        if (i < nj) {
           // S = Q K_i^T into place i & 1 (K = D in steps of 16: 4 per 64-channel box); the weights that
           // were there have been multiplied by an earlier product of this warp
-          const uint32_t place = 2 * h + (i & 1);
-          if (elect_one()) {
+          if (!(ok = warp_all(mbar_wait(b_full + 8 * t.at, t.ph, err, abort_flag)))) break;
+          tc_fence_after();
+          const uint32_t tile = t.at * Lay::kTile, place = 2 * h + (i & 1);
+          if (rows && elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               umma_step(tmem + Lay::kColS + place * kManyKeys, qd, (kk >> 2) * kRowBox + (kk & 3) * 32, kd,
-                        stage + (kk >> 2) * kKeyBox + (kk & 3) * 32, idesc_s, kk > 0 ? 1u : 0u);
+                        tile + (kk >> 2) * kKeyBox + (kk & 3) * 32, idesc_s, kk > 0 ? 1u : 0u);
             umma_commit(b_s + 8 * place);
           }
           __syncwarp();
+          release(b_empty + 8 * t.at);
+          if (i == nj - 1) release(b_qe);
+          t.next(S);
         }
-        if (i == nj - 1) release(b_qe);
-        if (rows && i > 0) {
+        if (i > 0) {
           // O += P V_{i-1}: K = 64 positions in steps of 16 (8 columns of P; two 8-row groups of V, the
           // next 64 channels one box on). The weights of a piece's first tile come after the last piece's
           // O has been read.
-          const uint32_t place = 2 * h + ((i - 1) & 1);
-          if (!(ok = warp_wait(b_p + 8 * place, pn >> place & 1, err, abort_flag))) break;
-          pn ^= 1u << place;
-          tc_fence_after();
-          if (elect_one()) {
+          const uint32_t tile = t.at * Lay::kTile, place = 2 * h + ((i - 1) & 1);
+          if (!(ok = warp_all(mbar_wait(b_full + 8 * t.at, t.ph, err, abort_flag)))) break;
+          if (rows) {
+            if (!(ok = warp_all(mbar_wait(b_p + 8 * place, pn >> place & 1, err, abort_flag)))) break;
+            pn ^= 1u << place;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kManyKeys / 16; ++kk)
-              umma_step_ta(o_col, tmem + Lay::kColS + place * kManyKeys + kk * 8, vd, stage + kk * 2048, idesc_pv,
-                           (i > 1 || kk > 0) ? 1u : 0u);
-            umma_commit(b_o + 8 * h);
-            if (i == nj) umma_commit(b_of + 8 * h);
+              for (int kk = 0; kk < kManyKeys / 16; ++kk)
+                umma_step_ta(o_col, tmem + Lay::kColS + place * kManyKeys + kk * 8, vd, tile + kk * 2048, idesc_pv,
+                             (i > 1 || kk > 0) ? 1u : 0u);
+              umma_commit(b_o + 8 * h);
+              if (i == nj) umma_commit(b_of + 8 * h);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          release(b_empty + 8 * t.at);
+          t.next(S);
         }
-        release(b_empty + 8 * t.at);
-        t.next(S);
       }
     }
     // every product issued above completes before tensor memory is released
@@ -1125,7 +1134,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const float c = mapped ? 1.f : a.scale_log2;
     const float slack = kRescaleSlack / c;
     const int rt = r / G, rg = r % G;
-    int stages = 0;          // of the ring, before this piece
+    int tiles = 0;           // of the ring, before this piece
     uint32_t sn = 0;         // bit `place`: turn of s_full
     int dn = 0, on = 0;      // products so far: of any tile, of a piece's last
     bool ok = true;
@@ -1134,7 +1143,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const int nj = p.j1 - p.j0;
       const int tok = h * tqh + rt;
       if (h == 1 && p.ntok <= tqh) {
-        stages += nj > 0 ? nj + 1 : 0;
+        tiles += 2 * nj;
         continue;
       }
       const Needed nd = needed_keys(p, hdr.window);
@@ -1204,14 +1213,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (!nd.all(k0, k0 + kManyKeys)) {
           // rows of V that no token sees may hold anything: their weight is zero, so make them zero
           // (both halves do, each ahead of its own product)
-          const int at = stages + j + 1;
+          const int at = tiles + (j + 1 < nj ? 2 * j + 2 : 2 * nj - 1);
           if (!warp_all(mbar_wait(b_full + 8 * (at % S), at / S & 1, err, abort_flag))) {
             ok = false;
             break;
           }
           if (!nd.at(k0 + (r >> 1))) {
-            const uint32_t vr =
-                base + Lay::kOffRing + (at % S) * Lay::kStage + Lay::kTile + (r >> 1) * 128 + (r & 1) * 64;
+            const uint32_t vr = base + Lay::kOffRing + (at % S) * Lay::kTile + (r >> 1) * 128 + (r & 1) * 64;
 #pragma unroll
             for (int bx = 0; bx < D / 64; ++bx)
 #pragma unroll
@@ -1231,7 +1239,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (lane == 0) mbar_arrive(b_p + 8 * place);
         ++dn;
       }
-      stages += nj > 0 ? nj + 1 : 0;
+      tiles += 2 * nj;
       if (!ok || (nj > 0 && !warp_all(mbar_wait(b_of + 8 * h, on++ & 1, err, abort_flag)))) {
         ok = false;
         break;
