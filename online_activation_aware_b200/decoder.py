@@ -54,15 +54,18 @@ class TTQDecoder:
                 rr = 0 if A is None else A.shape[0]
                 L["lin"][name] = ttq.TTQLinear(W["w_" + name], q, g, alpha, lam, 2, rr, A, B)
             self.layers.append(L)
-        n = len(self.layers)
-        self.k_cache = torch.empty(n, max_len, self.Hkv, self.D, dtype=torch.bfloat16, device=device)
-        self.v_cache = torch.empty_like(self.k_cache)
         self.table = ttq.rope_table(max_len, self.D, rope_base, device=device)
+        self._ws = {}
+        self._make_cache()
+
+    def _make_cache(self):
+        n, device = len(self.layers), self.device
+        self.k_cache = torch.empty(n, self.max_len, self.Hkv, self.D, dtype=torch.bfloat16, device=device)
+        self.v_cache = torch.empty_like(self.k_cache)
         self.length = 0
         self.pos = torch.zeros(1, dtype=torch.int64, device=device)   # next token's position
-        self.attn_ws = torch.empty(ttq.decode_attention_workspace_size(self.H, self.Hkv, self.D, max_len),
+        self.attn_ws = torch.empty(ttq.decode_attention_workspace_size(self.H, self.Hkv, self.D, self.max_len),
                                    dtype=torch.uint8, device=device)
-        self._ws = {}
         self._graph = None
 
     # -------------------------------------------------------------- buffers
@@ -78,19 +81,20 @@ class TTQDecoder:
     # -------------------------------------------------------------- the stack
 
     def _attention(self, li: int, qkv, T: int, prefill: bool):
-        H, D = self.H, self.D
+        """Attention of layer li from its stacked projection (q heads normalised and rotated in
+        place, k and v written to the cache). Returns (q, attention output)."""
+        H, D, nm = self.H, self.D, self.layers[li]["norms"]
+        ttq.qk_norm_rope(qkv, H, self.Hkv, D, nm["n_q"], nm["n_k"], self.eps, self.table, 0, self.k_cache[li],
+                         self.v_cache[li], pos0_dev=None if prefill else self.pos)
         if not prefill:
             # one token at the device-held position, over the cache up to and including it
-            return ttq.decode_attention(qkv, H, self.Hkv, D, self.k_cache[li], self.v_cache[li], pos_dev=self.pos,
-                                        ws=self.attn_ws).view(1, H * D)
-        return ttq.prompt_attention(qkv, H, self.Hkv, D, self.k_cache[li], self.v_cache[li])
+            return qkv[:, : H * D], ttq.decode_attention(qkv, H, self.Hkv, D, self.k_cache[li], self.v_cache[li],
+                                                         pos_dev=self.pos, ws=self.attn_ws).view(1, H * D)
+        return qkv[:, : H * D], ttq.prompt_attention(qkv, H, self.Hkv, D, self.k_cache[li], self.v_cache[li])
 
-    def _run(self, x, prefill: bool, trace=None):
+    def _stack(self, x, prefill: bool, trace=None):
+        """Every layer over the rows of x; returns the final-normed hidden states."""
         T = x.shape[0]
-        if not prefill and T != 1:
-            raise NotImplementedError("decode appends one token per call")
-        if prefill and T > self.max_len:
-            raise ValueError(f"{T} tokens exceed the cache of {self.max_len}")
         ws = self.workspace(T)
         r = x.clone()
         y = None
@@ -107,16 +111,14 @@ class TTQDecoder:
                 trace(li, "r_in", r)
                 trace(li, "h", h)
                 trace(li, "qkv", qkv)
-            ttq.qk_norm_rope(qkv, self.H, self.Hkv, self.D, nm["n_q"], nm["n_k"], self.eps, self.table, 0,
-                             self.k_cache[li], self.v_cache[li], pos0_dev=None if prefill else self.pos)
-            attn = self._attention(li, qkv, T, prefill)
+            q, attn = self._attention(li, qkv, T, prefill)
             o = step(attn, "o")
             h2 = ttq.rmsnorm(o, nm["n_post"], self.eps, residual=r)
             gu = step(h2, "gate_up")
             m = ttq.silu_mul(gu)
             y = step(m, "down")
             if trace:
-                trace(li, "q", qkv[:, : self.H * self.D])
+                trace(li, "q", q)
                 trace(li, "attn", attn)
                 trace(li, "o", o)
                 trace(li, "r_mid", r)
@@ -124,7 +126,15 @@ class TTQDecoder:
                 trace(li, "gu", gu)
                 trace(li, "m", m)
                 trace(li, "down", y)
-        out = ttq.rmsnorm(y, self.final_norm, self.eps, residual=r)
+        return ttq.rmsnorm(y, self.final_norm, self.eps, residual=r)
+
+    def _run(self, x, prefill: bool, trace=None):
+        T = x.shape[0]
+        if not prefill and T != 1:
+            raise NotImplementedError("decode appends one token per call")
+        if prefill and T > self.max_len:
+            raise ValueError(f"{T} tokens exceed the cache of {self.max_len}")
+        out = self._stack(x, prefill, trace)
         if prefill:
             self.pos.fill_(T)
         else:

@@ -1,0 +1,289 @@
+"""Several sequences that share one prompt: a cache made of pages and a decoder over it.
+
+TTQ's codes belong to a prompt: every layer is re-quantized from the prompt's own
+activations. Branches of a prompt (parallel samples, beams, alternative turns) therefore
+share its codes, and their decode steps run as rows of one TTQ linear. ``PagedCache`` gives
+them a key/value cache of pages, shared until a branch writes to one, and
+``PagedTTQDecoder`` is ``TTQDecoder`` over it: ``prefill`` a prompt, ``fork`` it, ``step``
+any of its sequences by one or several tokens each, ``score`` the answer.
+"""
+
+from __future__ import annotations
+
+import heapq
+
+import torch
+
+import online_activation_aware_b200 as ttq
+from online_activation_aware_b200.decoder import TTQDecoder
+
+
+class PagedCache:
+    """Key/value pools [layers, pages, page_size, kv_heads, head_dim] (bf16) and the pages of up
+    to ``max_seqs`` sequences of up to ``max_len`` positions.
+
+    The bookkeeping (free pages, how many sequences hold each page) lives on the host; the page
+    tables live on the device (``table`` [max_seqs, width] int32) and follow it. Pages that
+    several sequences hold are never written: ``extend`` gives a sequence its own copy of a
+    shared last page first. Every call acts on the current stream."""
+
+    def __init__(self, layers: int, pages: int, page_size: int, kv_heads: int, head_dim: int, max_seqs: int,
+                 max_len: int, device="cuda"):
+        if pages < 1 or max_seqs < 1 or max_len < 1:
+            raise ValueError("pages, max_seqs and max_len must be positive")
+        self.pages, self.page_size, self.max_seqs, self.max_len = pages, page_size, max_seqs, max_len
+        self.width = -(-max_len // page_size)
+        self.k = torch.empty(layers, pages, page_size, kv_heads, head_dim, dtype=torch.bfloat16, device=device)
+        self.v = torch.empty_like(self.k)
+        self.table = torch.full((max_seqs, self.width), -1, dtype=torch.int32, device=device)
+        self.clear()
+
+    def clear(self):
+        """Forgets every sequence."""
+        self._free = list(range(self.pages))       # a heap: the lowest page first
+        self._held = [0] * self.pages              # sequences that hold each page
+        self._pages = {}                           # sequence -> its pages
+        self._length = {}
+
+    @property
+    def free_pages(self) -> int:
+        return len(self._free)
+
+    @property
+    def sequences(self) -> list:
+        return sorted(self._pages)
+
+    def length(self, seq: int) -> int:
+        self._check(seq)
+        return self._length[seq]
+
+    def page_list(self, seq: int) -> list:
+        """The pages of a sequence, in order."""
+        self._check(seq)
+        return list(self._pages[seq])
+
+    def _check(self, seq):
+        if seq not in self._pages:
+            raise KeyError(f"no sequence {seq}")
+
+    def new(self) -> int:
+        """An empty sequence."""
+        for seq in range(self.max_seqs):
+            if seq not in self._pages:
+                self._pages[seq], self._length[seq] = [], 0
+                return seq
+        raise RuntimeError(f"all {self.max_seqs} sequences are in use")
+
+    def fork(self, seq: int) -> int:
+        """A new sequence with the same positions, sharing their pages."""
+        self._check(seq)
+        other = self.new()
+        self._pages[other] = list(self._pages[seq])
+        self._length[other] = self._length[seq]
+        for p in self._pages[seq]:
+            self._held[p] += 1
+        self.table[other].copy_(self.table[seq])
+        return other
+
+    def free(self, seq: int):
+        """Ends a sequence; pages that no other holds become free."""
+        self._check(seq)
+        for p in self._pages.pop(seq):
+            self._release(p)
+        del self._length[seq]
+
+    def truncate(self, seq: int, length: int):
+        """Drops the positions from ``length`` on (rejected tokens), with pages left without any."""
+        self._check(seq)
+        if not 0 <= length <= self._length[seq]:
+            raise ValueError(f"sequence {seq} has {self._length[seq]} positions")
+        keep = -(-length // self.page_size)
+        for p in self._pages[seq][keep:]:
+            self._release(p)
+        del self._pages[seq][keep:]
+        self._length[seq] = length
+
+    def _release(self, p):
+        self._held[p] -= 1
+        if self._held[p] == 0:
+            heapq.heappush(self._free, p)
+
+    def _upload(self, values):
+        """One host list of int32 values on the device, behind the current stream's work."""
+        return torch.tensor(values, dtype=torch.int32).to(self.table.device, non_blocking=True)
+
+    def extend(self, seqs, counts):
+        """Makes room for counts[i] more positions of sequence seqs[i]; shared pages that these
+        reach are copied first. Returns the step's device tensors (q_start, kv_len, page_table)."""
+        seqs, counts = list(seqs), list(counts)
+        if len(seqs) == 0 or len(set(seqs)) != len(seqs) or len(seqs) != len(counts):
+            raise ValueError("one count for each of at least one distinct sequences")
+        need = 0
+        for s, n in zip(seqs, counts):
+            self._check(s)
+            if n < 1:
+                raise ValueError("every sequence takes at least one token")
+            if self._length[s] + n > self.max_len:
+                raise ValueError(f"{self._length[s] + n} positions exceed {self.max_len}")
+            held = len(self._pages[s])
+            need += -(-(self._length[s] + n) // self.page_size) - held
+            if self._length[s] % self.page_size and self._held[self._pages[s][-1]] > 1:
+                need += 1
+        if need > len(self._free):
+            # (an upper bound: the last holder of a shared page keeps it)
+            raise RuntimeError(f"{need} pages are needed, {len(self._free)} are free")
+        src, dst, where = [], [], []
+        for s, n in zip(seqs, counts):
+            mine = self._pages[s]
+            if self._length[s] % self.page_size and self._held[mine[-1]] > 1:
+                p = heapq.heappop(self._free)
+                self._held[p] = 1
+                self._held[mine[-1]] -= 1
+                src.append(mine[-1])
+                dst.append(p)
+                mine[-1] = p
+                where.append((s, len(mine) - 1, p))
+            self._length[s] += n
+            while len(mine) * self.page_size < self._length[s]:
+                p = heapq.heappop(self._free)
+                self._held[p] = 1
+                mine.append(p)
+                where.append((s, len(mine) - 1, p))
+        # one upload: copies, table entries, the step's starts, lengths and rows (each part padded to
+        # 16 bytes)
+        starts = [0]
+        for n in counts:
+            starts.append(starts[-1] + n)
+        parts = [src, dst, [s * self.width + i for s, i, _ in where], [p for _, _, p in where], starts,
+                 [self._length[s] for s in seqs], seqs]
+        flat, at = [], []
+        for part in parts:
+            at.append(len(flat))
+            flat += part + [0] * (-len(part) % 4)
+        up = self._upload(flat)
+        src_d, dst_d, idx_d, new_d, start_d, len_d, row_d = (up[a: a + len(part)] for a, part in zip(at, parts))
+        if src:
+            ttq.copy_pages(self.k, self.v, src_d, dst_d)
+        if where:
+            self.table.view(-1).index_copy_(0, idx_d.long(), new_d)
+        return start_d, len_d, self.table.index_select(0, row_d)
+
+    def compact(self) -> int:
+        """Moves the held pages to the lowest places, so that the pools end in one run of free
+        pages; returns how many moved."""
+        held = [p for p in range(self.pages) if self._held[p]]
+        holes = [p for p in range(len(held)) if not self._held[p]]
+        movers = [p for p in held if p >= len(held)]
+        if not movers:
+            return 0
+        mapping = list(range(self.pages))
+        for p, h in zip(movers, holes):
+            mapping[p] = h
+            self._held[h], self._held[p] = self._held[p], 0
+        for s in self._pages:
+            self._pages[s] = [mapping[p] for p in self._pages[s]]
+        self._free = list(range(len(held), self.pages))
+        pad = -len(movers) % 4
+        up = self._upload(movers + [0] * pad + holes + [0] * pad + mapping)
+        n = len(movers) + pad
+        ttq.copy_pages(self.k, self.v, up[: len(movers)], up[n: n + len(movers)])
+        ttq.remap_pages(self.table, up[2 * n:], out=self.table)
+        return len(movers)
+
+
+class PagedTTQDecoder(TTQDecoder):
+    """``TTQDecoder`` whose sequences share one prompt and live in a ``PagedCache``.
+
+    ``prefill(x)`` starts a prompt (re-quantizing every layer; sequences of an earlier prompt
+    end) and leaves its sequence in ``prompt``; ``fork`` branches a sequence; ``step`` runs new
+    tokens of several sequences, one or more each, as the rows of one decode step with the
+    prompt's codes. With ``lm_head`` (bf16 [vocab, hidden]) the output head is one more TTQ
+    linear, and ``score`` gives log probabilities."""
+
+    def __init__(self, shape: dict, weights: list, final_norm, q: int, g: int, alpha: float, lam: float, r: int = 0,
+                 pages: int = 256, page_size: int = 64, max_seqs: int = 16, max_len: int = 4096 + 128, eps: float = 1e-6,
+                 rope_base: float = 1.0e6, lm_head=None, device="cuda"):
+        self._cache_args = (pages, page_size, max_seqs)
+        super().__init__(shape, weights, final_norm, q, g, alpha, lam, r, max_len, eps, rope_base, device)
+        self.lm_head = None if lm_head is None else ttq.TTQLinear(lm_head, q, g, alpha, lam)
+
+    def _make_cache(self):
+        pages, page_size, max_seqs = self._cache_args
+        self.cache = PagedCache(len(self.layers), pages, page_size, self.Hkv, self.D, max_seqs, self.max_len,
+                                self.device)
+        self.prompt = None
+        self._plans = {}
+
+    def _attention(self, li: int, qkv, T: int, prefill: bool):
+        start, length, pages, plan = self._step
+        nm, k, v = self.layers[li]["norms"], self.cache.k[li], self.cache.v[li]
+        q = ttq.qk_norm_rope_paged(qkv, self.H, self.Hkv, self.D, nm["n_q"], nm["n_k"], self.eps, self.table, start,
+                                   length, k, v, pages)
+        return q, ttq.paged_attention(q, plan, k, v, pages)
+
+    def _plan(self, seqs: int, tokens: int, longest: int):
+        key = (seqs, tokens, longest)
+        if key not in self._plans:
+            if len(self._plans) >= 16:
+                self._plans.clear()
+            self._plans[key] = ttq.AttentionPlan(seqs, tokens, self.H, self.Hkv, self.D, max_new=longest,
+                                                 device=self.device)
+        return self._plans[key]
+
+    def _run_step(self, x, seqs, counts, prefill: bool, trace=None):
+        start, length, pages = self.cache.extend(seqs, counts)
+        plan = self._plan(len(seqs), x.shape[0], max(counts)).update(start, length)
+        self._step = (start, length, pages, plan)
+        try:
+            return self._stack(x, prefill, trace)
+        finally:
+            self._step = None
+
+    def prefill(self, x, trace=None):
+        """Embeddings [T, hidden] bf16 of a new prompt -> final-normed hidden [T, hidden]; its
+        sequence is ``prompt``. Ends every sequence of the prompt before it."""
+        if x.shape[0] > self.max_len:
+            raise ValueError(f"{x.shape[0]} tokens exceed the cache of {self.max_len}")
+        if -(-x.shape[0] // self.cache.page_size) > self.cache.pages:
+            raise RuntimeError(f"{x.shape[0]} tokens exceed {self.cache.pages} pages of {self.cache.page_size}")
+        self.cache.clear()
+        self.prompt = self.cache.new()
+        return self._run_step(x, [self.prompt], [x.shape[0]], True, trace)
+
+    def step(self, seqs, x, counts=None, trace=None):
+        """New tokens' embeddings x [sum counts, hidden], counts[i] (default one) of sequence
+        seqs[i] -> their final-normed hidden states."""
+        if self.prompt is None:
+            raise RuntimeError("step needs a prefill first")
+        seqs = list(seqs)
+        counts = [1] * len(seqs) if counts is None else list(counts)
+        if sum(counts) != x.shape[0]:
+            raise ValueError(f"{x.shape[0]} rows for {sum(counts)} tokens")
+        return self._run_step(x, seqs, counts, False, trace)
+
+    def decode(self, x, trace=None):
+        """The next token of the prompt's own sequence."""
+        if self.prompt is None:
+            raise RuntimeError("decode needs a prefill first")
+        return self.step([self.prompt], x, None, trace)
+
+    def capture_decode(self):
+        raise NotImplementedError("steps of a paged decoder take their pages from the host")
+
+    def fork(self, seq: int | None = None, count: int = 1) -> list:
+        """``count`` new sequences that continue ``seq`` (default: the prompt's)."""
+        if self.prompt is None:
+            raise RuntimeError("fork needs a prefill first")
+        return [self.cache.fork(self.prompt if seq is None else seq) for _ in range(count)]
+
+    def free(self, seq: int):
+        self.cache.free(seq)
+
+    def score(self, hidden, tokens, top: int = 0, prefill: bool = False):
+        """Log probabilities of ``tokens`` (int64, one a row of the final-normed hidden states),
+        entropies and the ``top`` alternatives, through the output head. ``prefill`` quantizes
+        the head from these rows (a prompt's); later calls reuse its codes."""
+        if self.lm_head is None:
+            raise RuntimeError("the decoder has no output head")
+        logits = self.lm_head.prefill(hidden) if prefill else self.lm_head.decode(hidden)
+        return ttq.token_logprobs(logits, tokens, top)
