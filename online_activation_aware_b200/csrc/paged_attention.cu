@@ -14,8 +14,9 @@
 //   few_rows_kernel  at most 16 rows a sequence (single tokens): memory bound. Four warps take 16
 //                    keys each of every 64-key tile on mma.sync, each with its own running
 //                    softmax, merged at the end of a piece;
-//   many_rows_kernel tiles of up to 256 rows on tcgen05;
-//   merge_kernel     joins the pieces of a split tile.
+//   many_rows_kernel tiles of up to 256 rows on tcgen05.
+// The pieces of a split tile leave partial results, and the block that leaves the last one joins
+// them (in the order of the pieces, whichever block that is, so that results repeat bit for bit).
 // Scores, maxima, sums and accumulators are fp32; the weights are rounded to bf16 for the second
 // product.
 // Every mbarrier wait is bounded: a CTA that gives up records TTQ_ERR_TIMEOUT, drains what it
@@ -23,7 +24,6 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
-#include <type_traits>
 
 #include "attention_common.cuh"
 #include "ttq_internal.h"
@@ -58,10 +58,11 @@ struct __align__(16) Piece {
   int slot;             // where its partial result goes (-1: it is the whole tile)
   int pre;              // prefix of the sequence
   int kvh;              // key/value head
-  int pad;
+  int split;            // of a partial result
 };
-struct Split {
-  int tok0, ntok, slot0, pieces, kvh, pad[3];
+// A tile (and key/value head) of more than one piece; arrived counts those that are done, by half.
+struct __align__(16) Split {
+  int slot0, pieces, arrived[2];
 };
 
 // Sizes that follow from the shape alone (same on the host and the device).
@@ -134,8 +135,8 @@ __device__ __forceinline__ TileKeys tile_keys(int p0, int ntok, int pre, int win
 }
 
 // Units of work of a tile with that many key tiles: starting and finishing one costs about as much
-// as two key tiles.
-__device__ __forceinline__ int tile_cost(int total) { return total + 2; }
+// as two key tiles of few rows, or five of many (5.5 us).
+__device__ __forceinline__ int tile_cost(int total, bool few) { return total + (few ? 2 : 5); }
 
 __device__ __forceinline__ uint64_t warp_scan(uint64_t x) {
 #pragma unroll
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
     uint64_t cost = 0, tot;
     if (t < ntiles) {
       Piece p;
-      cost = static_cast<uint64_t>(tile_cost(tile_of(t, &p).total)) * h.kv_heads;
+      cost = static_cast<uint64_t>(tile_cost(tile_of(t, &p).total, l.rows == kFewRows)) * h.kv_heads;
     }
     const uint64_t at = work + block_scan(cost, &tot, sh, turn);
     if (t < ntiles) tile_at[t] = at;
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
       const int t = i / h.kv_heads;
       p.kvh = i - t * h.kv_heads;
       k = tile_of(t, &p);
-      cost = tile_cost(k.total);
+      cost = tile_cost(k.total, l.rows == kFewRows);
       a = tile_at[t] + static_cast<uint64_t>(p.kvh) * cost;
       c0 = divide(a, share, inv_share);
       np = static_cast<int>(divide(a + cost - 1, share, inv_share) - c0 + 1);
@@ -277,7 +278,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
     base += tot;
     const int first = static_cast<int>(here >> 32), slot0 = static_cast<int>(here >> 16 & 0xffff);
     const int split = static_cast<int>(here & 0xffff);
-    if (np > 1 && split < l.max_splits) splits[split] = Split{p.tok0, p.ntok, slot0, np, p.kvh, {0, 0, 0}};
+    if (np > 1 && split < l.max_splits) splits[split] = Split{slot0, np, {0, 0}};
+    p.split = split;
     const float keys = static_cast<float>(k.total) / static_cast<float>(cost);  // key tiles per unit
     auto key_at = [&](int x) { return x == cost ? k.total : min(k.total, static_cast<int>(static_cast<float>(x) * keys)); };
     for (int n = 0; n < np; ++n) {
@@ -311,7 +313,7 @@ struct PagedArgs {
   PlanHeader want;  // the shape this call was given
   const uint8_t* plan;
   size_t off_cta, off_pieces, off_splits;
-  float* acc;       // partial accumulators [slot][row][D], unnormalised
+  float* acc;       // partial accumulators, unnormalised: [slot][row][D] (few rows), [slot][D / 4][row][4]
   float2* ml;       // their (maximum in log2 units, sum)
   int row_cap, G, stages;
   const int* table;
@@ -330,6 +332,10 @@ struct PagedArgs {
 __device__ __forceinline__ bool plan_ok(const PlanHeader& h, const PlanHeader& w) {
   return h.magic == kPlanMagic && h.seqs == w.seqs && h.tokens == w.tokens && h.max_new == w.max_new &&
          h.heads == w.heads && h.kv_heads == w.kv_heads && h.head_dim == w.head_dim;
+}
+
+__device__ __forceinline__ Split* split_of(const PagedArgs& a, const Piece& p) {
+  return reinterpret_cast<Split*>(const_cast<uint8_t*>(a.plan) + a.off_splits) + p.split;
 }
 
 // Scores in log2 units from a raw product: scale, cap, bias. tanh by its exponential form
@@ -487,7 +493,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
   using Lay = FewLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bar_full[kFewMaxStages], bar_empty[kFewMaxStages];
-  __shared__ int abort_sh;
+  __shared__ int abort_sh, last_sh;
   __shared__ float m_sh[4][kFewRows], l_sh[4][kFewRows];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -745,6 +751,55 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
           if (c == 0) a.ml[row] = make_float2(M, Ls);
         }
       }
+      if (p.slot >= 0) {
+        Split* sp = split_of(a, p);
+        __threadfence();  // the partial result ahead of its arrival
+        few_any(false);
+        if (threadIdx.x == 0) last_sh = atomicAdd(&sp->arrived[0], 1) == sp->pieces - 1;
+        few_any(false);
+        if (last_sh) {
+          __threadfence();
+          const int np = sp->pieces;
+          const int64_t row0 = static_cast<int64_t>(sp->slot0) * a.row_cap;
+          for (int i = threadIdx.x; i < rows * (D / 4); i += 128) {
+            const int r = i / (D / 4), c = i % (D / 4) * 4;
+            float M = -FLT_MAX, Ls = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            // eight pieces at a time, their loads in flight together
+            for (int n0 = 0; n0 < np; n0 += 8) {
+              float2 ml[8];
+              float4 v[8];
+              float m8 = M;
+#pragma unroll
+              for (int n = 0; n < 8; ++n) {
+                const int64_t row = row0 + static_cast<int64_t>(min(n0 + n, np - 1)) * a.row_cap + r;
+                ml[n] = __ldcg(a.ml + row);
+                v[n] = __ldcg(reinterpret_cast<const float4*>(a.acc + row * D + c));
+              }
+#pragma unroll
+              for (int n = 0; n < 8; ++n)
+                if (n0 + n < np) m8 = fmaxf(m8, ml[n].x);
+              const float f0 = exp2_approx(M - m8);
+              M = m8;
+              Ls *= f0;
+              acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+#pragma unroll
+              for (int n = 0; n < 8; ++n)
+                if (n0 + n < np) {
+                  const float f = exp2_approx(ml[n].x - M);
+                  Ls = fmaf(ml[n].y, f, Ls);
+                  acc = make_float4(fmaf(v[n].x, f, acc.x), fmaf(v[n].y, f, acc.y), fmaf(v[n].z, f, acc.z),
+                                    fmaf(v[n].w, f, acc.w));
+                }
+            }
+            const float inv = Ls > 0.f ? __fdiv_rn(1.f, Ls) : 0.f;
+            __nv_bfloat16* dst = a.out + static_cast<int64_t>(p.tok0 + r / G) * a.ld_out + (p.kvh * G + r % G) * D + c;
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          }
+          if (threadIdx.x == 0) sp->arrived[0] = 0;  // for the next layer on this plan
+        }
+      }
       few_any(false);  // the exchange is rewritten by the next piece
     }
   }
@@ -774,6 +829,7 @@ struct ManyBars {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
+  int last[2];                 // a half's piece is the last of its tile to be done
 };
 
 // smem: Q of both halves | ring of tiles K_0, K_1 V_0, K_2 V_1, ..., V_last, in 1024-byte aligned
@@ -909,6 +965,32 @@ __device__ __forceinline__ void map_scores(uint32_t (&sr)[kManyKeys], const Scor
     sr[k] = __float_as_uint(r.x);
     sr[k + 1] = __float_as_uint(r.y);
   }
+}
+
+// 32 columns of a row of O; zeros where the piece had no key tile.
+template <int D>
+__device__ __forceinline__ void load_o(uint32_t to, int cc, bool any, uint32_t (&o)[32]) {
+  if (any) {
+    tmem_ld_32x32b_x32(to + 32 * cc, o);
+    tmem_ld_wait();
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = 0u;
+  }
+}
+
+// The four softmax warps of a half meet; true when `v` is true of any of them.
+__device__ __forceinline__ bool half_any(int h, bool v) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 128, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(1 + h), "r"(v ? 1 : 0)
+      : "memory");
+  return r != 0;
 }
 
 // A place in a ring of n, and its turn.
@@ -1138,7 +1220,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     uint32_t sn = 0;         // bit `place`: turn of s_full
     int dn = 0, on = 0;      // products so far: of any tile, of a piece's last
     bool ok = true;
-    for (int pi = range.x; ok && pi < range.y; ++pi) {
+    for (int pi = range.x; pi < range.y; ++pi) {
       const Piece p = load_piece(a, pi);
       const int nj = p.j1 - p.j0;
       const int tok = h * tqh + rt;
@@ -1240,26 +1322,81 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         ++dn;
       }
       tiles += 2 * nj;
-      if (!ok || (nj > 0 && !warp_all(mbar_wait(b_of + 8 * h, on++ & 1, err, abort_flag)))) {
-        ok = false;
-        break;
-      }
+      ok = ok && (nj == 0 || warp_all(mbar_wait(b_of + 8 * h, on++ & 1, err, abort_flag)));
+      if (half_any(h, !ok)) break;  // a wait ran out in some warp: all four leave
       tc_fence_after();
-      const float inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
       __nv_bfloat16* orow = a.out + static_cast<int64_t>(p.tok0 + tok) * a.ld_out + head * D;
+      // a partial result: [slot][D / 4][row][4], a warp's stores of four channels next to each other
       const int64_t prow = static_cast<int64_t>(p.slot) * a.row_cap + h * kHalfRows + r;
+      float4* part = reinterpret_cast<float4*>(a.acc) + static_cast<int64_t>(p.slot) * a.row_cap * (D / 4) + h * kHalfRows + r;
+      bool last = p.slot < 0;
+      Split* sp = nullptr;
+      if (p.slot >= 0) {
 #pragma unroll 1
-      for (int cc = 0; cc < D / 32; ++cc) {
-        uint32_t o[32];
-        if (nj > 0) {
-          tmem_ld_32x32b_x32(to + 32 * cc, o);
-          tmem_ld_wait();
-        } else {
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o[32];
+          load_o<D>(to, cc, nj > 0, o);
+          if (real) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
+            for (int q4 = 0; q4 < 8; ++q4)
+              part[static_cast<int64_t>(8 * cc + q4) * a.row_cap] =
+                  make_float4(__uint_as_float(o[4 * q4]), __uint_as_float(o[4 * q4 + 1]), __uint_as_float(o[4 * q4 + 2]),
+                              __uint_as_float(o[4 * q4 + 3]));
+          }
         }
-        if (!real) continue;
-        if (p.slot < 0) {
+        if (real) a.ml[prow] = make_float2(m * c, l);
+        sp = split_of(a, p);
+        __threadfence();  // the partial result ahead of its arrival
+        half_any(h, false);
+        if (quad == 0 && lane == 0) bars->last[h] = atomicAdd(&sp->arrived[h], 1) == sp->pieces - 1;
+        half_any(h, false);
+        last = bars->last[h];
+        if (last) __threadfence();
+      }
+      if (last) {
+        // the whole row, of this piece alone or of all pieces in their order
+        const int np = sp != nullptr ? sp->pieces : 1, slot0 = sp != nullptr ? sp->slot0 : p.slot;
+        const float2* mls = a.ml + static_cast<int64_t>(slot0) * a.row_cap + h * kHalfRows + r;
+        const float4* parts =
+            reinterpret_cast<const float4*>(a.acc) + static_cast<int64_t>(slot0) * a.row_cap * (D / 4) + h * kHalfRows + r;
+        float M = m * c, Ls = l;
+        if (sp != nullptr && real) {
+          for (int n = 0; n < np; ++n) M = fmaxf(M, __ldcg(mls + static_cast<int64_t>(n) * a.row_cap).x);
+          Ls = 0.f;
+          for (int n = 0; n < np; ++n) {
+            const float2 ml = __ldcg(mls + static_cast<int64_t>(n) * a.row_cap);
+            Ls = fmaf(ml.y, exp2_approx(ml.x - M), Ls);
+          }
+        }
+        const float inv = Ls > 0.f ? __fdiv_rn(1.f, Ls) : 0.f;
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o[32];
+          load_o<D>(to, cc, nj > 0, o);
+          if (!real) continue;
+          if (sp != nullptr) {
+            float acc[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+#pragma unroll 1
+            for (int n = 0; n < np; ++n) {
+              const float f = exp2_approx(__ldcg(mls + static_cast<int64_t>(n) * a.row_cap).x - M);
+              const bool own = slot0 + n == p.slot;
+              const float4* src = parts + (static_cast<int64_t>(n) * (D / 4) + 8 * cc) * a.row_cap;
+#pragma unroll
+              for (int q4 = 0; q4 < 8; ++q4) {
+                const float4 v = own ? make_float4(__uint_as_float(o[4 * q4]), __uint_as_float(o[4 * q4 + 1]),
+                                                   __uint_as_float(o[4 * q4 + 2]), __uint_as_float(o[4 * q4 + 3]))
+                                     : __ldcg(src + static_cast<int64_t>(q4) * a.row_cap);
+                acc[4 * q4] = fmaf(v.x, f, acc[4 * q4]);
+                acc[4 * q4 + 1] = fmaf(v.y, f, acc[4 * q4 + 1]);
+                acc[4 * q4 + 2] = fmaf(v.z, f, acc[4 * q4 + 2]);
+                acc[4 * q4 + 3] = fmaf(v.w, f, acc[4 * q4 + 3]);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(acc[e]);
+          }
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {
             uint32_t w[4];
@@ -1269,14 +1406,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                                  __fmul_rn(__uint_as_float(o[8 * q4 + 2 * e + 1]), inv));
             *reinterpret_cast<uint4*>(orow + 32 * cc + 8 * q4) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        } else {
-#pragma unroll
-          for (int q4 = 0; q4 < 8; ++q4)
-            *reinterpret_cast<uint4*>(a.acc + prow * D + 32 * cc + 4 * q4) =
-                make_uint4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
-          if (cc == 0) a.ml[prow] = make_float2(m * c, l);
         }
+        if (sp != nullptr && quad == 0 && lane == 0) sp->arrived[h] = 0;  // for the next layer on this plan
       }
+      tc_fence_before();  // O has been read ahead of the weights that let the next piece overwrite it
     }
   }
   tc_fence_before();
@@ -1287,80 +1420,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   }
 }
 
-// ---------------------------------------------------------------- joining the pieces of a tile
-
-// Blocks walk the rows of the split tiles. TEAM (few rows, possibly many pieces): a row a block,
-// every warp taking every eighth piece, then joined; else a row a warp.
-template <int D, bool TEAM>
-__global__ void __launch_bounds__(256) merge_kernel(const PagedArgs a) {
-  constexpr int E = D / 32;
-  using Vec = typename std::conditional<E == 4, float4, float2>::type;
-  __shared__ float m_sh[8], l_sh[8];
-  __shared__ float acc_sh[TEAM ? 8 : 1][D];
-  pdl_enter();
-  const PlanHeader hdr = *reinterpret_cast<const PlanHeader*>(a.plan);
-  if (!plan_ok(hdr, a.want)) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = TEAM ? 1 : 8;  // rows a block takes at once
-  const int steps = (a.row_cap + per - 1) / per;
-  for (int64_t w = blockIdx.x; w < static_cast<int64_t>(hdr.splits) * steps; w += gridDim.x) {
-    const Split s = reinterpret_cast<const Split*>(a.plan + a.off_splits)[w / steps];
-    const int r = static_cast<int>(w % steps) * per + (TEAM ? 0 : warp);
-    // the row's token and head (rows of a tcgen05 half are padded to kHalfRows)
-    const int half = TEAM ? 0 : r / kHalfRows, rr = TEAM ? r : r % kHalfRows;
-    const int tqh = kHalfRows / a.G;
-    const int tok = half * tqh + rr / a.G;
-    if (tok >= s.ntok || (!TEAM && rr / a.G >= tqh)) continue;  // (the same for all that meet below)
-    const int64_t row = static_cast<int64_t>(s.slot0) * a.row_cap + r;
-    const int first = TEAM ? warp : 0, step = TEAM ? 8 : 1;
-    float M = -FLT_MAX;
-    for (int i = TEAM ? threadIdx.x : lane; i < s.pieces; i += TEAM ? 256 : 32)
-      M = fmaxf(M, a.ml[row + static_cast<int64_t>(i) * a.row_cap].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (TEAM) {
-      if (lane == 0) m_sh[warp] = M;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) M = fmaxf(M, m_sh[i]);
-    }
-    float acc[E], l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int i = first; i < s.pieces; i += step) {
-      const int64_t at = row + static_cast<int64_t>(i) * a.row_cap;
-      const float2 ml = a.ml[at];
-      const float f = exp2_approx(ml.x - M);
-      const Vec v = *reinterpret_cast<const Vec*>(a.acc + at * D + lane * E);
-      l = fmaf(ml.y, f, l);
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(reinterpret_cast<const float*>(&v)[e], f, acc[e]);
-    }
-    __nv_bfloat16* dst = a.out + static_cast<int64_t>(s.tok0 + tok) * a.ld_out + (s.kvh * a.G + rr % a.G) * D;
-    if (TEAM) {
-      if (lane == 0) l_sh[warp] = l;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc_sh[warp][lane * E + e] = acc[e];
-      __syncthreads();
-      if (threadIdx.x < D) {
-        float ls = 0.f, v = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ls += l_sh[i];
-          v += acc_sh[i][threadIdx.x];
-        }
-        dst[threadIdx.x] = __float2bfloat16_rn(ls > 0.f ? __fdiv_rn(v, ls) : 0.f);
-      }
-      __syncthreads();  // the exchange is rewritten by the next row
-    } else {
-      const float inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
-#pragma unroll
-      for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t*>(dst + lane * E + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    }
-  }
-}
+// ---------------------------------------------------------------- launches
 
 PlanHeader plan_header(const PagedShape& s, int64_t window) {
   PlanHeader h = {};
@@ -1382,7 +1442,7 @@ cudaError_t prepare_kernel(K kernel, size_t smem) {
 }
 
 template <int D>
-cudaError_t launch_attention_d(PagedArgs a, const PagedShape& s, const PagePool& p, const PlanLayout& l, int num_sms,
+cudaError_t launch_attention_d(PagedArgs a, const PagedShape& s, const PagePool& p, const PlanLayout& l,
                                cudaStream_t stream) {
   const uint64_t positions = static_cast<uint64_t>(p.num_pages) * p.page_size;
   const uint64_t s1 = D * 2, s2 = static_cast<uint64_t>(s.kv_heads) * D * 2;
@@ -1398,9 +1458,7 @@ cudaError_t launch_attention_d(PagedArgs a, const PagedShape& s, const PagePool&
     a.stages = FewLayout<D>::stages(l.row_cap);
     e = prepare_kernel(few_rows_kernel<D>, smem);
     if (e == cudaSuccess) e = launch_pdl(few_rows_kernel<D>, grid, dim3(kFewThreads), smem, stream, tk, tv, a);
-    if (e != cudaSuccess) return e;
-    const int blocks = std::min(l.max_splits * l.row_cap, num_sms * 8);
-    return launch_pdl(merge_kernel<D, true>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, a);
+    return e;
   }
   CUtensorMap tq;
   if (!encode_bf16_tmap_3d(&tq, a.q, D, s.heads, s.tokens, D * 2, static_cast<uint64_t>(a.ld_q) * 2, 64,
@@ -1409,8 +1467,7 @@ cudaError_t launch_attention_d(PagedArgs a, const PagedShape& s, const PagePool&
   e = prepare_kernel(many_rows_kernel<D>, ManyLayout<D>::kSmem);
   if (e == cudaSuccess)
     e = launch_pdl(many_rows_kernel<D>, grid, dim3(kManyThreads), ManyLayout<D>::kSmem, stream, tq, tk, tv, a);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(merge_kernel<D, false>, dim3(static_cast<unsigned>(num_sms * 8)), dim3(256), 0, stream, a);
+  return e;
 }
 
 }  // namespace
@@ -1451,8 +1508,7 @@ cudaError_t launch_paged_attention(const void* q, int64_t ld_q, const PagedShape
   a.ld_out = static_cast<int>(s.heads * s.head_dim);
   a.out = static_cast<__nv_bfloat16*>(out);
   a.err = err;
-  return s.head_dim == 64 ? launch_attention_d<64>(a, s, p, l, num_sms, stream)
-                          : launch_attention_d<128>(a, s, p, l, num_sms, stream);
+  return s.head_dim == 64 ? launch_attention_d<64>(a, s, p, l, stream) : launch_attention_d<128>(a, s, p, l, stream);
 }
 
 }  // namespace ttq
