@@ -388,7 +388,7 @@ TTQ_API ttq_status ttq_paged_attention(const void* q_bf16, int64_t ld_q, int64_t
                                        float softcap, const float* slopes, void* out_bf16, void* plan,
                                        size_t plan_bytes, cudaStream_t stream);
 
-/* ttq_qk_norm_rope for a paged cache: the same arithmetic, with every token's position and
+/* ttq_qk_norm_rope for a paged cache: the same results (to the order of a sum), with every token's position and
  * pages taken from its sequence, and q written to its own buffer (qkv is only read).
  *   qkv       device bf16 [tokens, (heads + 2 kv_heads) * head_dim]
  *   q_out     device bf16 [tokens, heads * head_dim], not overlapping qkv

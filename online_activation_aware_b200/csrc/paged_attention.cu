@@ -37,6 +37,7 @@ constexpr int kHalfRows = 128;     // rows of one tcgen05 block; many_rows_kerne
 constexpr int kManyKeys = 64;      // its key tile
 constexpr int kPlanThreads = 256;   // (1024 took twice as long: the idle ones run the scans too)
 constexpr int kPlanTiles = 2048;   // tiles whose data the plan keeps in shared memory
+constexpr int kPlanCtas = 1024;    // blocks a plan can cut the work for
 constexpr unsigned kPlanMagic = 0x54545133u;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -88,7 +89,7 @@ PlanLayout plan_layout(const PagedShape& s, int num_sms) {
   l.tq = static_cast<int>(few ? kFewRows / G : 2 * (kHalfRows / G));
   l.row_cap = few ? static_cast<int>(s.max_new * G) : 2 * kHalfRows;
   l.key_tile = few ? kFewKeys : kManyKeys;
-  l.ctas = num_sms * (few ? 2 : 1);
+  l.ctas = std::min(num_sms * (few ? 2 : 1), kPlanCtas);
   l.max_tiles = static_cast<int>(std::min(s.tokens, s.tokens / l.tq + s.seqs));
   // every cut adds one piece, and at most two of the pieces of a split tile
   l.max_pieces = static_cast<int>(l.max_tiles * s.kv_heads + l.ctas);
@@ -135,8 +136,11 @@ __device__ __forceinline__ TileKeys tile_keys(int p0, int ntok, int pre, int win
 }
 
 // Units of work of a tile with that many key tiles: starting and finishing one costs about as much
-// as two key tiles of few rows, or five of many (5.5 us).
-__device__ __forceinline__ int tile_cost(int total, bool few) { return total + (few ? 2 : 5); }
+// as two key tiles of few rows, or eight of many.
+__device__ __forceinline__ int tile_cost(int total, bool few) { return total + (few ? 2 : 8); }
+// A cut this near to the end of a tile moves there: writing and joining partial results costs as
+// much again.
+__device__ __forceinline__ int cut_slack(bool few) { return few ? 2 : 6; }
 
 __device__ __forceinline__ uint64_t warp_scan(uint64_t x) {
 #pragma unroll
@@ -176,6 +180,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
   int turn = 0;
   __shared__ int2 tile_seq_sh[kPlanTiles];
   __shared__ uint64_t tile_at_sh[kPlanTiles];
+  __shared__ int cta_first_sh[kPlanCtas];
   pdl_enter();
   const int tid = threadIdx.x;
   PlanHeader* out = reinterpret_cast<PlanHeader*>(plan);
@@ -254,46 +259,53 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
   // equal shares; a share shorter than a few key tiles is not worth its start
   const uint64_t share = max(static_cast<uint64_t>(4), (work + l.ctas - 1) / l.ctas);
   const float inv_share = 1.f / static_cast<float>(share);
+  for (int c = tid; c < l.ctas; c += kPlanThreads) cta_first_sh[c] = 0x7fffffff;
+  __syncthreads();
   // pieces of every item (tile, kv head), scanned as (pieces, slots, splits) in 32 + 16 + 16 bits
   const int items = ntiles * h.kv_heads;
   uint64_t base = 0;
   for (int i0 = 0; i0 < items; i0 += kPlanThreads) {
     const int i = i0 + tid;
     Piece p = {};
-    TileKeys k = {};
+    int total = 0, cost = 1, np = 0;
     uint64_t a = 0, v = 0, tot;
     uint32_t c0 = 0;
-    int np = 0, cost = 1;
     if (i < items) {
       const int t = i / h.kv_heads;
       p.kvh = i - t * h.kv_heads;
-      k = tile_of(t, &p);
-      cost = tile_cost(k.total, l.rows == kFewRows);
+      total = tile_of(t, &p).total;
+      cost = tile_cost(total, l.rows == kFewRows);
       a = tile_at[t] + static_cast<uint64_t>(p.kvh) * cost;
-      c0 = divide(a, share, inv_share);
-      np = static_cast<int>(divide(a + cost - 1, share, inv_share) - c0 + 1);
+      // cuts up to `slack` inside the item move to its ends; those between cut it
+      const int slack = min(cut_slack(l.rows == kFewRows), cost / 2);
+      c0 = divide(a + slack, share, inv_share);
+      np = static_cast<int>(max(c0, divide(a + cost - slack - 1, share, inv_share)) - c0 + 1);
       v = static_cast<uint64_t>(np) << 32 | (np > 1 ? static_cast<uint64_t>(np) << 16 | 1u : 0u);
     }
     const uint64_t here = base + block_scan(v, &tot, sh, turn);
     base += tot;
     const int first = static_cast<int>(here >> 32), slot0 = static_cast<int>(here >> 16 & 0xffff);
-    const int split = static_cast<int>(here & 0xffff);
-    if (np > 1 && split < l.max_splits) splits[split] = Split{slot0, np, {0, 0}};
-    p.split = split;
-    const float keys = static_cast<float>(k.total) / static_cast<float>(cost);  // key tiles per unit
-    auto key_at = [&](int x) { return x == cost ? k.total : min(k.total, static_cast<int>(static_cast<float>(x) * keys)); };
+    p.split = static_cast<int>(here & 0xffff);
+    if (np > 1 && p.split < l.max_splits) splits[p.split] = Split{slot0, np, {0, 0}};
+    const float keys = static_cast<float>(total) / static_cast<float>(cost);  // key tiles per unit
+    auto key_at = [&](uint64_t x) { return min(total, static_cast<int>(static_cast<float>(x - a) * keys)); };
+    p.j1 = 0;
     for (int n = 0; n < np; ++n) {
-      const uint64_t lo = max(a, (c0 + n) * share) - a, hi = min(a + cost, (c0 + n + 1) * share) - a;
-      p.j0 = key_at(static_cast<int>(lo));
-      p.j1 = key_at(static_cast<int>(hi));
+      p.j0 = p.j1;
+      p.j1 = n == np - 1 ? total : key_at((c0 + n + 1) * share);
       p.slot = np > 1 ? slot0 + n : -1;
       if (first + n < l.max_pieces) pieces[first + n] = p;
-      if (a + lo == (c0 + n) * share) cta_first[c0 + n] = first + n;  // (c0 + n < ctas: share covers the work)
+      atomicMin(&cta_first_sh[c0 + n], first + n);  // (c0 + n < ctas: the shares cover the work)
     }
   }
   const int npieces = static_cast<int>(base >> 32);
-  for (uint64_t c = (work + share - 1) / share + tid; c <= static_cast<uint64_t>(l.ctas); c += kPlanThreads)
-    cta_first[c] = npieces;
+  __syncthreads();
+  const int used = work > 0 ? static_cast<int>(divide(work - 1, share, inv_share)) + 1 : 0;
+  for (int c = tid; c <= l.ctas; c += kPlanThreads) {
+    int n = c;  // (a block whose cuts moved together has no pieces: it ends where the next begins)
+    while (n < used && cta_first_sh[n] == 0x7fffffff) ++n;
+    cta_first[c] = n < used ? cta_first_sh[n] : npieces;
+  }
   if (tid == 0) {
     h.magic = kPlanMagic;
     h.pieces = npieces;

@@ -815,7 +815,7 @@ ttq_status ttq_qk_norm_rope_paged(const void* qkv_bf16, int64_t seqs, int64_t to
   ttq_status st = check_pool(p, seqs);
   if (st != TTQ_OK) return st;
   if (!std::isfinite(eps) || !(eps > 0.f)) return TTQ_ERR_INVALID_ARG;
-  if (tokens * (heads + 2 * kv_heads) >= (int64_t(1) << 34)) return TTQ_ERR_TOO_LARGE;  // blocks of one grid
+  if (tokens * (heads + 2 * kv_heads) >= (int64_t(1) << 31)) return TTQ_ERR_TOO_LARGE;  // groups of one grid
   if (!aligned16(qkv_bf16) || !aligned16(q_norm_bf16) || !aligned16(k_norm_bf16) || !aligned16(rope_table) ||
       !aligned16(q_start) || !aligned16(kv_len) || !aligned16(q_out_bf16))
     return TTQ_ERR_MISALIGNED;

@@ -309,7 +309,7 @@ def test_page_write(H, Hkv, D, page, new, length):
     assert torch.equal(vd.view(torch.int16), c.vd.view(torch.int16))
 
 
-def test_page_write_gives_the_dense_cache_bits():
+def test_page_write_gives_the_dense_cache():
     T, H, Hkv, D = 77, 8, 2, 128
     rng = np.random.default_rng(8)
     qkv = synthetic.as_bf16(rng.normal(size=(T, (H + 2 * Hkv) * D))).cuda()
@@ -321,9 +321,11 @@ def test_page_write_gives_the_dense_cache_bits():
                                i32([[3, 1, 5, 0, 2, 4]]))
     dense = qkv.clone()
     ttq.qk_norm_rope(dense, H, Hkv, D, wq, wk, 1e-6, rope, 9, kc, vc)
-    assert torch.equal(q, dense[:, : H * D])
+    # the two kernels add a head's 128 squares in different orders, so their fp32 results differ by up
+    # to 128 * 2^-24 of themselves and may round to neighbouring bf16 values, no further
+    assert_ulp(q, vals(dense[:, : H * D]), 2.0 ** -19)
     order = torch.tensor([3, 1, 5, 0, 2, 4])
-    assert torch.equal(kp[order].reshape(96, Hkv, D)[: T + 9], kc[: T + 9])
+    assert_ulp(kp[order].reshape(96, Hkv, D)[: T + 9], vals(kc[: T + 9]), 2.0 ** -19)
     assert torch.equal(vp[order].reshape(96, Hkv, D)[: T + 9], vc[: T + 9])
 
 
