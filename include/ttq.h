@@ -24,7 +24,8 @@
  *     errors are returned synchronously and nothing is launched. A failed launch returns
  *     TTQ_ERR_CUDA. A kernel that gives up on a bounded wait records TTQ_ERR_TIMEOUT in
  *     the device error word, which ttq_device_status() reports.
- *   - Alignment: every pointer must be 16-byte aligned (TTQ_ERR_MISALIGNED otherwise).
+ *   - Alignment: every pointer must be 16-byte aligned (TTQ_ERR_MISALIGNED otherwise), where an
+ *     entry point does not ask for less.
  *   - Supported settings: q in {2,3,4}; g in {32,64,128}; d % g == 0; p in {1,2};
  *     alpha >= 0; lambda > 0 when alpha > 0; 0 <= r <= 64 with A and B non-NULL
  *     exactly when r > 0.
@@ -347,7 +348,8 @@ TTQ_API ttq_status ttq_prompt_attention(const void* qkv_bf16, int64_t T, int64_t
  * A value read on the device that is out of range (a table entry that is no page, lengths
  * that contradict the sizes given here) makes no access outside the buffers;
  * ttq_device_status() then reports TTQ_ERR_INVALID_ARG and the rows concerned are
- * unspecified. page_size in {16, 32, 64, 128, 256}; num_pages * page_size < 2^31.
+ * unspecified. page_size in {16, 32, 64, 128, 256}; num_pages * page_size < 2^31. The int32 and
+ * int64 arrays (and fp32 slopes) need no more than their own alignment.
  * --------------------------------------------------------------------------------- */
 
 /* Plan of one step's attention, used by every layer of the step: the split of the work over
@@ -378,7 +380,7 @@ TTQ_API ttq_status ttq_attention_plan(const int32_t* q_start, const int32_t* kv_
  * the plan. A token that sees no position (kv_len below the number of new tokens) gets zeros.
  *   q        device bf16, row t at q + t * ld_q elements, its first heads * head_dim
  *            channels (ld_q % 8 == 0)
- *   slopes   NULL, or device fp32 [heads]
+ *   softcap  0, or at least 1e-30;  slopes   NULL, or device fp32 [heads]
  *   out      device bf16 [tokens, heads * head_dim], not overlapping q
  * k and v at visible positions must be finite; what pages hold past kv_len is never used. */
 TTQ_API ttq_status ttq_paged_attention(const void* q_bf16, int64_t ld_q, int64_t seqs, int64_t tokens,
@@ -388,8 +390,9 @@ TTQ_API ttq_status ttq_paged_attention(const void* q_bf16, int64_t ld_q, int64_t
                                        float softcap, const float* slopes, void* out_bf16, void* plan,
                                        size_t plan_bytes, cudaStream_t stream);
 
-/* ttq_qk_norm_rope for a paged cache: the same results (to the order of a sum), with every token's position and
- * pages taken from its sequence, and q written to its own buffer (qkv is only read).
+/* ttq_qk_norm_rope for a paged cache: the same results (to the order of a sum), with every
+ * token's position and pages taken from its sequence, and q written to its own buffer (qkv is
+ * only read).
  *   qkv       device bf16 [tokens, (heads + 2 kv_heads) * head_dim]
  *   q_out     device bf16 [tokens, heads * head_dim], not overlapping qkv
  *   rope_table device fp32 from ttq_rope_table; a position past its table_positions rows, or
@@ -425,7 +428,7 @@ typedef enum { TTQ_BF16 = 0, TTQ_FP16 = 1, TTQ_FP32 = 2 } ttq_dtype;
  *   logprob[r] = log p[tokens[r]]   (0 where tokens[r] < 0: a padding row)
  *   entropy[r] = -sum p log p       (nats)
  *   top_ids[r], top_logprobs[r]     in falling order, equal logits by rising index
- *   logits   device, row r at element r * ld (ld >= vocab), of type `dtype`; 16-byte aligned base
+ *   logits   device, row r at element r * ld (ld >= vocab), of type `dtype`, aligned to it
  *   tokens   device int64 [rows]; a token past the vocabulary gives NaN and is reported by
  *            ttq_device_status()
  *   top_ids  device int64 [rows, top], top_logprobs device fp32 [rows, top]; NULL when top = 0

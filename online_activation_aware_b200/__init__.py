@@ -583,6 +583,16 @@ def _same_device(*named):
     return _OnDevice(index)
 
 
+def _fresh(stream, like, shape, dtype=None):
+    """A new tensor beside ``like``, from the memory of the stream that will use it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _queue(stream, guard):
     """Handle of the given stream, or of the current one of the guarded device."""
     if stream is not None:
@@ -678,9 +688,9 @@ def paged_attention(q, plan: AttentionPlan, k_pages, v_pages, page_table, softca
     with _same_device(("q", q), ("k_pages", k_pages), ("v_pages", v_pages), ("page_table", page_table),
                       ("slopes", slopes), ("out", out), ("plan", plan.buffer)) as on:
         if out is None:
-            out = q.new_empty((T, H * D))
+            out = _fresh(stream, q, (T, H * D))
         _check("ttq_paged_attention", load_library().ttq_paged_attention(
-            q.data_ptr(), q.stride(0) if T > 1 else q.shape[1], plan.seqs, T, plan.max_new, H, plan.kv_heads, D,
+            q.data_ptr(), q.stride(0) if T > 1 else H * D, plan.seqs, T, plan.max_new, H, plan.kv_heads, D,
             _address(k_pages, bfloat16, "k_pages"), _address(v_pages, bfloat16, "v_pages"), pages, page_size,
             _address(page_table, int32, "page_table"), width, softcap, _address(slopes, float32, "slopes"),
             _address(out, bfloat16, "out"), plan.buffer.data_ptr(), plan.buffer.numel(), _queue(stream, on)))
@@ -709,7 +719,7 @@ def qk_norm_rope_paged(qkv, heads: int, kv_heads: int, head_dim: int, q_norm, k_
                       ("kv_len", kv_len), ("k_pages", k_pages), ("v_pages", v_pages), ("page_table", page_table),
                       ("q", q)) as on:
         if q is None:
-            q = qkv.new_empty((T, heads * head_dim))
+            q = _fresh(stream, qkv, (T, heads * head_dim))
         _check("ttq_qk_norm_rope_paged", load_library().ttq_qk_norm_rope_paged(
             _address(qkv, bfloat16, "qkv"), seqs, T, heads, kv_heads, head_dim, _address(q_norm, bfloat16, "q_norm"),
             _address(k_norm, bfloat16, "k_norm"), eps, _address(table, float32, "table"), table.shape[0],
@@ -753,7 +763,7 @@ def remap_pages(table, mapping, out=None, stream=None):
     _shape(out, "out", tuple(table.shape))
     with _same_device(("table", table), ("mapping", mapping), ("out", out)) as on:
         if out is None:
-            out = table.new_empty(table.shape)
+            out = _fresh(stream, table, table.shape)
         _check("ttq_remap_pages", load_library().ttq_remap_pages(
             _address(table, int32, "table"), table.numel(), _address(mapping, int32, "mapping"), mapping.shape[0],
             _address(out, int32, "out"), _queue(stream, on)))
@@ -781,13 +791,13 @@ def token_logprobs(logits, tokens, top: int = 0, ws=None, stream=None):
         _check("ttq_token_logprobs_workspace_size",
                lib.ttq_token_logprobs_workspace_size(rows, vocab, top, ctypes.byref(n)))
         if ws is None and n.value > 0:
-            ws = logits.new_empty(n.value, dtype=torch.uint8)
-        out = {"logprob": logits.new_empty(rows, dtype=torch.float32),
-               "entropy": logits.new_empty(rows, dtype=torch.float32)}
+            ws = _fresh(stream, logits, n.value, torch.uint8)
+        out = {"logprob": _fresh(stream, logits, rows, torch.float32),
+               "entropy": _fresh(stream, logits, rows, torch.float32)}
         ids = lps = None
         if top > 0:
-            ids = out["top_ids"] = logits.new_empty((rows, top), dtype=torch.int64)
-            lps = out["top_logprobs"] = logits.new_empty((rows, top), dtype=torch.float32)
+            ids = out["top_ids"] = _fresh(stream, logits, (rows, top), torch.int64)
+            lps = out["top_logprobs"] = _fresh(stream, logits, (rows, top), torch.float32)
         _check("ttq_token_logprobs", lib.ttq_token_logprobs(
             logits.data_ptr(), kind, rows, vocab, logits.stride(0) if rows > 1 else vocab,
             _address(tokens, torch.int64, "tokens"), top, out["logprob"].data_ptr(), out["entropy"].data_ptr(),

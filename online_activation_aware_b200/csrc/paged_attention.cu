@@ -350,21 +350,40 @@ __device__ __forceinline__ Split* split_of(const PagedArgs& a, const Piece& p) {
   return reinterpret_cast<Split*>(const_cast<uint8_t*>(a.plan) + a.off_splits) + p.split;
 }
 
-// Scores in log2 units from a raw product: scale, cap, bias. tanh by its exponential form
-// 1 - 2 / (e^{2x} + 1): off by a few 2^-24 of the cap, where the hardware's tanh would be off by
-// 2^-11 of it (a tenth of a unit in the exponent at a cap of 50).
+// tanh x = x Q(x^2) for |x| <= 1, by the polynomial of least relative error (6e-7).
+__device__ __forceinline__ constexpr float tanh_coef(int i) {
+  return i == 0   ? 0.9999994040f
+         : i == 1 ? -0.3332904279f
+         : i == 2 ? 0.1328143328f
+         : i == 3 ? -0.0516056754f
+         : i == 4 ? 0.0167431161f
+                  : -0.0030670604f;
+}
+
+// A raw product to its score in log2 units, capped: cap tanh(s / cap), which is s Q((s / cap)^2)
+// inside the cap and cap (1 - 2 / (e^{2 s / cap} + 1)) beyond it. (The hardware's tanh is off by 2^-11
+// of the cap, a tenth of a unit in the exponent at a cap of 50; the exponential form alone by 2^-23 of
+// it, which a large cap would feel.)
 struct ScoreMap {
-  float scale, cap2, arg;  // log2(e) / sqrt(D); cap log2(e); 2 log2(e) / (cap sqrt(D))
+  float scale, cap2, unit;  // log2(e) / sqrt(D); cap log2(e); 1 / (cap sqrt(D))
   __device__ __forceinline__ float operator()(float s) const {
-    if (cap2 > 0.f) return cap2 - __fdividef(2.f * cap2, exp2_approx(s * arg) + 1.f);
-    return s * scale;
+    if (!(cap2 > 0.f)) return s * scale;
+    const float x = s * unit;
+    if (fabsf(x) <= 1.f) {
+      const float z = x * x;
+      float q = tanh_coef(5);
+#pragma unroll
+      for (int i = 4; i >= 0; --i) q = fmaf(q, z, tanh_coef(i));
+      return s * scale * q;
+    }
+    return cap2 - __fdividef(2.f * cap2, exp2_approx(x * (2.f * kLog2e)) + 1.f);
   }
 };
 __device__ __forceinline__ ScoreMap score_map(const PagedArgs& a) {
   ScoreMap m;
   m.scale = a.scale_log2;
   m.cap2 = a.cap * kLog2e;
-  m.arg = a.cap > 0.f ? 2.f * a.scale_log2 / a.cap : 0.f;
+  m.unit = a.cap > 0.f ? a.scale_log2 / (a.cap * kLog2e) : 0.f;
   return m;
 }
 
@@ -940,9 +959,8 @@ __device__ __forceinline__ float weights(uint32_t (&sr)[kManyKeys], float c, flo
   return s.x + s.y;
 }
 
-// Raw products to scores in log2 units: cap and bias of a row whose first key is at distance d0.
-// tanh x = x Q(x^2) with the polynomial of least relative error (6e-7) for x^2 <= 1, which covers
-// scores up to the cap; a warp that meets a larger one takes tanh's exponential form.
+// Raw products to scores in log2 units, capped and biased, of a row whose first key is at distance
+// d0: two at a time inside the cap; a warp that meets a score beyond it takes them one by one.
 __device__ __forceinline__ void map_scores(uint32_t (&sr)[kManyKeys], const ScoreMap& map, float slope, float d0,
                                            bool real) {
   float big = 0.f;
@@ -951,9 +969,8 @@ __device__ __forceinline__ void map_scores(uint32_t (&sr)[kManyKeys], const Scor
     for (int k = 0; k < kManyKeys; k += 2)
       big = fmaxf(fmaxf(big, fabsf(__uint_as_float(sr[k]))), fabsf(__uint_as_float(sr[k + 1])));
   }
-  const float unit = map.arg * 0.34657359f;  // x = s * unit (arg is 2 log2(e) of it)
-  const uint64_t slope2 = pack2(slope, slope), scale2 = pack2(map.scale, map.scale), unit2 = pack2(unit, unit);
-  if (map.cap2 > 0.f && __any_sync(0xffffffffu, real && !(big * unit <= 1.f))) {
+  const uint64_t slope2 = pack2(slope, slope), scale2 = pack2(map.scale, map.scale), unit2 = pack2(map.unit, map.unit);
+  if (map.cap2 > 0.f && __any_sync(0xffffffffu, real && !(big * map.unit <= 1.f))) {
 #pragma unroll
     for (int k = 0; k < kManyKeys; ++k)
       sr[k] = __float_as_uint(fmaf(slope, d0 + static_cast<float>(k), map(__uint_as_float(sr[k]))));
@@ -966,11 +983,9 @@ __device__ __forceinline__ void map_scores(uint32_t (&sr)[kManyKeys], const Scor
     uint64_t v = mul2(s, scale2);
     if (capped) {
       const uint64_t x = mul2(s, unit2), z = mul2(x, x);
-      uint64_t q = fma2(z, pack2(-0.0030670604f, -0.0030670604f), pack2(0.0167431161f, 0.0167431161f));
-      q = fma2(q, z, pack2(-0.0516056754f, -0.0516056754f));
-      q = fma2(q, z, pack2(0.1328143328f, 0.1328143328f));
-      q = fma2(q, z, pack2(-0.3332904279f, -0.3332904279f));
-      q = fma2(q, z, pack2(0.9999994040f, 0.9999994040f));
+      uint64_t q = pack2(tanh_coef(5), tanh_coef(5));
+#pragma unroll
+      for (int i = 4; i >= 0; --i) q = fma2(q, z, pack2(tanh_coef(i), tanh_coef(i)));
       v = mul2(v, q);
     }
     const float2 r = unpack2(fma2(pack2(d0 + static_cast<float>(k), d0 + static_cast<float>(k + 1)), slope2, v));

@@ -709,6 +709,9 @@ ttq_status ttq_prompt_attention(const void* qkv_bf16, int64_t T, int64_t heads, 
 }
 
 namespace {
+// int32 and int64 arrays of the paged entry points need no more than their own alignment.
+inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 ttq_status check_paged(const ttq::PagedShape& s) {
   if (s.head_dim != 64 && s.head_dim != 128) return TTQ_ERR_UNSUPPORTED;
   if (s.heads < 1 || s.kv_heads < 1 || s.heads > 1024 || s.heads % s.kv_heads != 0) return TTQ_ERR_INVALID_ARG;
@@ -726,7 +729,7 @@ ttq_status check_pool(const ttq::PagePool& p, int64_t seqs) {
   if (p.num_pages < 1 || p.num_pages >= (int64_t(1) << 31) / p.page_size || p.width < 1 ||
       p.width > (int64_t(1) << 30) / seqs)
     return TTQ_ERR_INVALID_ARG;
-  if (!aligned16(p.k) || !aligned16(p.v) || !aligned16(p.table)) return TTQ_ERR_MISALIGNED;
+  if (!aligned16(p.k) || !aligned16(p.v) || !aligned4(p.table)) return TTQ_ERR_MISALIGNED;
   return TTQ_OK;
 }
 // SM count of the current device; without one (sizes asked for on the host) the B200's.
@@ -738,7 +741,6 @@ int sms_or_default() {
 bool grid_fits(const ttq::PagedShape& s) {
   return (s.tokens + s.seqs + 8192) * s.kv_heads < (int64_t(1) << 31);
 }
-inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 }  // namespace
 
 ttq_status ttq_attention_plan_size(int64_t seqs, int64_t tokens, int64_t max_new, int64_t heads, int64_t kv_heads,
@@ -762,7 +764,7 @@ ttq_status ttq_attention_plan(const int32_t* q_start, const int32_t* kv_len, con
   if (!grid_fits(s)) return TTQ_ERR_TOO_LARGE;
   if (window < 0 || window > (int64_t(1) << 30)) return TTQ_ERR_INVALID_ARG;
   if (!plan || plan_bytes < ttq::attention_plan_bytes(s, sms_or_default())) return TTQ_ERR_WORKSPACE;
-  if (!aligned16(q_start) || !aligned16(kv_len) || (prefix && !aligned16(prefix)) || !aligned16(plan))
+  if (!aligned4(q_start) || !aligned4(kv_len) || (prefix && !aligned4(prefix)) || !aligned16(plan))
     return TTQ_ERR_MISALIGNED;
   DeviceInfo* di = nullptr;
   st = device_info(&di);
@@ -785,11 +787,11 @@ ttq_status ttq_paged_attention(const void* q_bf16, int64_t ld_q, int64_t seqs, i
   st = check_pool(p, seqs);
   if (st != TTQ_OK) return st;
   if (ld_q < heads * head_dim || ld_q > (int64_t(1) << 30)) return TTQ_ERR_INVALID_ARG;
-  if (!std::isfinite(softcap) || softcap < 0.f) return TTQ_ERR_INVALID_ARG;
+  if (!std::isfinite(softcap) || (softcap != 0.f && !(softcap >= 1e-30f))) return TTQ_ERR_INVALID_ARG;
   if (!grid_fits(s)) return TTQ_ERR_TOO_LARGE;
   if (!plan || plan_bytes < ttq::attention_plan_bytes(s, sms_or_default())) return TTQ_ERR_WORKSPACE;
   if (!aligned16(q_bf16) || ld_q % 8 != 0 || !aligned16(out_bf16) || !aligned16(plan) ||
-      (slopes && !aligned16(slopes)))
+      (slopes && !aligned4(slopes)))
     return TTQ_ERR_MISALIGNED;
   DeviceInfo* di = nullptr;
   st = device_info(&di);
@@ -817,7 +819,7 @@ ttq_status ttq_qk_norm_rope_paged(const void* qkv_bf16, int64_t seqs, int64_t to
   if (!std::isfinite(eps) || !(eps > 0.f)) return TTQ_ERR_INVALID_ARG;
   if (tokens * (heads + 2 * kv_heads) >= (int64_t(1) << 31)) return TTQ_ERR_TOO_LARGE;  // groups of one grid
   if (!aligned16(qkv_bf16) || !aligned16(q_norm_bf16) || !aligned16(k_norm_bf16) || !aligned16(rope_table) ||
-      !aligned16(q_start) || !aligned16(kv_len) || !aligned16(q_out_bf16))
+      !aligned4(q_start) || !aligned4(kv_len) || !aligned16(q_out_bf16))
     return TTQ_ERR_MISALIGNED;
   DeviceInfo* di = nullptr;
   st = device_info(&di);
@@ -835,7 +837,7 @@ ttq_status ttq_copy_pages(void* k_pool, void* v_pool, int64_t layers, int64_t nu
       page_bytes > (int64_t(1) << 30) || pairs < 1 || pairs > num_pages)
     return TTQ_ERR_INVALID_ARG;
   if (pairs * ((page_bytes >> 14) + 1) >= (int64_t(1) << 31)) return TTQ_ERR_TOO_LARGE;
-  if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(src) || !aligned16(dst) || page_bytes % 16 != 0)
+  if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned4(src) || !aligned4(dst) || page_bytes % 16 != 0)
     return TTQ_ERR_MISALIGNED;
   DeviceInfo* di = nullptr;
   const ttq_status st = device_info(&di);
@@ -849,7 +851,7 @@ ttq_status ttq_remap_pages(const int32_t* table, int64_t entries, const int32_t*
   if (!table || !mapping || !out || out == mapping) return TTQ_ERR_INVALID_ARG;
   if (entries < 1 || entries > (int64_t(1) << 31) - 256 || num_pages < 1 || num_pages > (int64_t(1) << 30))
     return TTQ_ERR_INVALID_ARG;
-  if (!aligned16(table) || !aligned16(mapping) || !aligned16(out)) return TTQ_ERR_MISALIGNED;
+  if (!aligned4(table) || !aligned4(mapping) || !aligned4(out)) return TTQ_ERR_MISALIGNED;
   DeviceInfo* di = nullptr;
   const ttq_status st = device_info(&di);
   if (st != TTQ_OK) return st;
@@ -884,8 +886,10 @@ ttq_status ttq_token_logprobs(const void* logits, ttq_dtype dtype, int64_t rows,
     return TTQ_ERR_INVALID_ARG;
   const size_t need = ttq::token_logprobs_ws_bytes(rows, vocab, top, sms_or_default());
   if (need > 0 && (!ws || ws_bytes < need)) return TTQ_ERR_WORKSPACE;
-  if (!aligned16(logits) || !aligned8(tokens) || !aligned16(logprob) || !aligned16(entropy) ||
-      (top_ids && !aligned16(top_ids)) || (top_logprobs && !aligned16(top_logprobs)) || (ws && !aligned16(ws)))
+  const uintptr_t elem = dtype == TTQ_FP32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(logits) % elem != 0 || !aligned8(tokens) || !aligned4(logprob) ||
+      !aligned4(entropy) || (top_ids && !aligned8(top_ids)) || (top_logprobs && !aligned4(top_logprobs)) ||
+      (ws && !aligned16(ws)))
     return TTQ_ERR_MISALIGNED;
   DeviceInfo* di = nullptr;
   st = device_info(&di);

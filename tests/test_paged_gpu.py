@@ -208,6 +208,56 @@ def test_strided_queries_and_shared_pages():
     assert ttq.device_status() == 0
 
 
+@pytest.mark.parametrize("softcap", [1e-3, 1e6, 3e38])
+@pytest.mark.parametrize("max_new", [1, None])
+def test_extreme_caps(softcap, max_new):
+    # a cap that flattens every score, and caps too large to matter
+    check(Case([1, 1] if max_new else [1, 40], [200, 90], 8, 2, 128, 16, seed=4), max_new=max_new, softcap=softcap)
+
+
+def test_padding_rows_and_neighbours_do_not_leak():
+    # NaN in the padding rows of q and in another sequence's own cache stays where it is
+    c = Case([3, 20, 1], [40, 300, 17], 8, 2, 128, 16, seed=12, pad=5)
+    c.qd[24:] = float("nan")
+    c.kd[c.table[0][0]] = float("nan")
+    c.vd[c.table[0][0]] = float("inf")
+    out = torch.full((c.N, 8 * 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    ttq.paged_attention(c.qd, c.plan(), c.kd, c.vd, c.td, out=out)
+    want, mag = c.want()
+    assert_attention(out[3:24], want[3:], mag[3:])
+    assert torch.all(out[24:] == 7.0) and ttq.device_status() == 0
+
+
+def test_lists_at_any_alignment_and_a_wide_single_row():
+    c = Case([1], [77], 8, 2, 64, 16, pad=0, seed=13)
+    off = lambda t: torch.cat([t.new_zeros(3), t.reshape(-1)])[3:].view(t.shape)
+    wide = torch.zeros(1, 8 * 64 + 5, dtype=torch.bfloat16, device="cuda")
+    wide[:, : 8 * 64] = c.qd
+    p = ttq.AttentionPlan(1, 1, 8, 2, 64).update(off(c.start), off(c.ld), prefix=off(i32([4])))
+    out = ttq.paged_attention(wide, p, c.kd, c.vd, off(c.td), slopes=off(torch.full((8,), 0.1, device="cuda")))
+    assert_attention(out, *c.want(prefix=[4], slopes=[0.1] * 8))
+    assert ttq.device_status() == 0
+
+
+def test_calls_on_another_stream():
+    c = Case([1, 40], [300, 90], 8, 2, 128, 16, seed=14)
+    side = torch.cuda.Stream()
+    plan = ttq.AttentionPlan(2, c.N, 8, 2, 128)
+    side.wait_stream(torch.cuda.current_stream())
+    plan.update(c.start, c.ld, stream=side)
+    out = ttq.paged_attention(c.qd, plan, c.kd, c.vd, c.td, stream=side)
+    x = torch.randn(5, 9000, device="cuda")
+    tok = torch.arange(5, device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    got = ttq.token_logprobs(x, tok, 3, stream=side)
+    junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(8)]   # reuses freed memory, if any
+    side.synchronize()
+    assert_attention(out, *c.want())
+    want = ttq.token_logprobs(x, tok, 3)
+    assert all(torch.equal(got[k], want[k]) for k in want) and len(junk) == 8
+    assert ttq.device_status() == 0
+
+
 def test_results_repeat_bit_for_bit():
     c = Case([1, 5, 64, 1], [3000, 900, 4000, 17], 8, 2, 128, 64, seed=21)
     first = check(c)
@@ -476,6 +526,8 @@ def test_token_logprobs_strided_rows_and_bad_tokens():
     wide[:, :1001] = torch.randn(9, 1001, device="cuda")
     for dtype in (torch.float32, torch.bfloat16, torch.float16):
         check_logprobs(wide.to(dtype)[:, :1001], torch.arange(9, device="cuda"), 10)
+    for dtype in (torch.float32, torch.bfloat16):           # rows and columns of a larger tensor
+        check_logprobs(torch.randn(9, 5001, device="cuda").to(dtype)[3:, 7:], torch.arange(6, device="cuda"), 10)
     x = torch.randn(3, 100, device="cuda")
     got = ttq.token_logprobs(x, torch.tensor([100, 1, 2 ** 40], device="cuda"))
     assert torch.isnan(got["logprob"][[0, 2]]).all() and torch.isfinite(got["logprob"][1])

@@ -59,8 +59,9 @@ def test_plan_errors(lib):
     assert plan(seqs=0) == INVALID
     assert plan(ws=0) == WORKSPACE
     assert plan(wsb=nb - 256) == WORKSPACE
-    assert plan(start=A + 4) == MISALIGNED
-    assert plan(prefix=C + 8) == MISALIGNED
+    assert plan(start=A + 2) == MISALIGNED
+    assert plan(prefix=C + 2) == MISALIGNED
+    assert plan(ws=W + 8) == MISALIGNED
 
 
 def test_attention_errors(lib):
@@ -81,8 +82,11 @@ def test_attention_errors(lib):
     assert att(ld=4100) == MISALIGNED
     assert att(cap=-1.0) == INVALID and att(cap=float("nan")) == INVALID and att(cap=float("inf")) == INVALID
     assert att(ws=0) == WORKSPACE and att(wsb=16) == WORKSPACE
-    for name in ("q", "k", "v", "table", "out", "ws", "slopes"):
+    assert att(cap=1e-38) == INVALID
+    for name in ("q", "k", "v", "out", "ws"):
         assert att(**{name: 7 * (1 << 20) + 8}) == MISALIGNED
+    for name in ("table", "slopes"):
+        assert att(**{name: 7 * (1 << 20) + 2}) == MISALIGNED
 
 
 def test_page_write_errors(lib):
@@ -94,7 +98,7 @@ def test_page_write_errors(lib):
     assert app(D=96) == UNSUPPORTED and app(page=12) == UNSUPPORTED
     assert app(seqs=0) == INVALID and app(tokens=0) == INVALID and app(heads=0) == INVALID and app(rows=0) == INVALID
     assert app(eps=0.0) == INVALID and app(out=Q) == INVALID and app(v=A) == INVALID and app(start=0) == INVALID
-    assert app(qkv=Q + 2) == MISALIGNED and app(out=O + 8) == MISALIGNED and app(start=A + 4) == MISALIGNED
+    assert app(qkv=Q + 2) == MISALIGNED and app(out=O + 8) == MISALIGNED and app(start=A + 2) == MISALIGNED
 
 
 def test_page_copy_and_remap_errors(lib):
@@ -104,13 +108,13 @@ def test_page_copy_and_remap_errors(lib):
     assert copy(k=0) == INVALID and copy(v=A) == INVALID and copy(src=0) == INVALID
     assert copy(layers=0) == INVALID and copy(pages=0) == INVALID and copy(n=0) == INVALID and copy(n=11) == INVALID
     assert copy(nb=0) == INVALID
-    assert copy(nb=4104) == MISALIGNED and copy(k=A + 8) == MISALIGNED and copy(dst=Q + 4) == MISALIGNED
+    assert copy(nb=4104) == MISALIGNED and copy(k=A + 8) == MISALIGNED and copy(dst=Q + 2) == MISALIGNED
 
     def remap(table=A, n=10, m=B, pages=5, out=C):
         return lib.ttq_remap_pages(P(table), n, P(m), pages, P(out), None)
 
     assert remap(table=0) == INVALID and remap(n=0) == INVALID and remap(pages=0) == INVALID and remap(out=B) == INVALID
-    assert remap(m=B + 4) == MISALIGNED
+    assert remap(m=B + 2) == MISALIGNED
 
 
 def test_logprob_errors(lib):
@@ -128,7 +132,8 @@ def test_logprob_errors(lib):
     assert lp(dt=3) == UNSUPPORTED and lp(top=33) == UNSUPPORTED
     assert lp(rows=0) == INVALID and lp(vocab=0) == INVALID and lp(ld=999) == INVALID and lp(top=-1) == INVALID
     assert lp(ids=0) == INVALID and lp(tl=0) == INVALID and lp(top=0) == INVALID
-    assert lp(x=A + 2) == MISALIGNED and lp(tok=B + 4) == MISALIGNED and lp(tl=W + 8) == MISALIGNED
+    assert lp(x=A + 1) == MISALIGNED and lp(x=A + 2, dt=2) == MISALIGNED
+    assert lp(tok=B + 4) == MISALIGNED and lp(tl=W + 2) == MISALIGNED and lp(ws=(7 << 20) + 8) in (MISALIGNED, -5)
 
 
 def test_binding_refuses_wrong_tensors(lib):
