@@ -432,15 +432,12 @@ typedef enum { TTQ_BF16 = 0, TTQ_FP16 = 1, TTQ_FP32 = 2 } ttq_dtype;
  *   tokens   device int64 [rows]; a token past the vocabulary gives NaN and is reported by
  *            ttq_device_status()
  *   top_ids  device int64 [rows, top], top_logprobs device fp32 [rows, top]; NULL when top = 0
- *   ws       device scratch of ttq_token_logprobs_workspace_size() bytes
  * A logit of -inf is a token of probability zero. A row with a NaN or +inf logit, or with
  * nothing but -inf, has NaN probabilities and entropy; its top_ids stay in the order of its
  * logits, NaN after everything else. 0 <= top <= min(32, vocab); vocab <= 2^20; rows < 2^31. */
-TTQ_API ttq_status ttq_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int64_t top, size_t* bytes);
 TTQ_API ttq_status ttq_token_logprobs(const void* logits, ttq_dtype dtype, int64_t rows, int64_t vocab, int64_t ld,
                                       const int64_t* tokens, int64_t top, float* logprob, float* entropy,
-                                      int64_t* top_ids, float* top_logprobs, void* ws, size_t ws_bytes,
-                                      cudaStream_t stream);
+                                      int64_t* top_ids, float* top_logprobs, cudaStream_t stream);
 
 /* *pos_dev += n on the device, in stream order (moves a captured decode step to the next
  * position). */

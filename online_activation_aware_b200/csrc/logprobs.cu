@@ -13,8 +13,8 @@
 // first one (a merge of two sorted lists of 32 is six shuffles), so that about 5 `top` keys a row
 // are ever inserted. A chunk whose maximum is below the threshold costs one comparison a thread.
 //
-// Memory bound: one read of the logits. Few rows are split over several blocks (segments), whose
-// sums and candidates a second kernel joins.
+// Memory bound: one read of the logits. Few rows are split over the blocks of a cluster (segments),
+// whose first block reads the others' sums and candidates from their shared memory.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -31,7 +31,7 @@ constexpr int kStages = 3;       // chunks in flight, the one at work included
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = kVecs * kThreads;  // vectors of a chunk
 constexpr int kMaxTop = 32;      // one key a lane
-constexpr int kMaxSegments = 64;
+constexpr int kMaxSegments = 16;  // blocks of a cluster
 constexpr float kLog2e = 1.4426950408889634f;
 
 // A 16-byte vector of N logits: pair i as two floats, and the largest of kVecs vectors (a NaN is
@@ -212,15 +212,25 @@ __device__ __forceinline__ void write_top(const Outs& o, int64_t r, int top, con
   o.top_lp[r * top + threadIdx.x] = (key_value(static_cast<unsigned>(k >> 32)) - a.m) - log_sum(a);
 }
 
-// One block per (row, segment). ONE: the row's only segment.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The word at the same place of shared memory in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t remote_word(const void* local, int rank) {
+  uint32_t at, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// One block per (row, segment); the segments of a row are a cluster. ONE: the row's only segment.
 template <typename T, bool TOP, bool ONE>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kernel(const T* __restrict__ logits, int vocab, int64_t ld,
-                                                                    int segments, int top, Outs o, Sums* parts,
-                                                                    Key* part_keys) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+    token_logprobs_kernel(const T* __restrict__ logits, int vocab, int64_t ld, int segments, int top, Outs o) {
   constexpr int N = Vec<T>::N;
   __shared__ Key lists[2][kWarps][32];  // the warps' lists, by turns
-  extern __shared__ uint4 ring[];          // [kStages][kVecs][kThreads]
-  __shared__ Key tau_sh;  // a key that at least `top` of the block's reach
+  extern __shared__ uint4 ring[];       // [kStages][kVecs][kThreads]
+  __shared__ Key tau_sh;                // a key that at least `top` of the block's reach
   pdl_enter();
   const int tid = threadIdx.x;
   const int64_t r = ONE ? blockIdx.x : blockIdx.x / segments;
@@ -363,86 +373,93 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
   }
   if (TOP) gather();
   a = block_join(a);
-  if (tid == 0) {
-    if (ONE) write_row(o, r, a, x, vocab);
-    else parts[blockIdx.x] = a;
+  if (ONE) {
+    if (tid == 0) write_row(o, r, a, x, vocab);
+    if (TOP && tid < top) write_top(o, r, top, a, mine);
+    return;
   }
-  if (TOP && tid < top) {
-    if (ONE) write_top(o, r, top, a, mine);
-    else part_keys[static_cast<int64_t>(blockIdx.x) * top + tid] = mine;
+  __shared__ Sums part;
+  __shared__ Key part_keys[32];
+  if (tid == 0) part = a;
+  if (TOP && warp == 0) part_keys[lane] = mine;
+  cluster_sync();
+  if (seg == 0) {
+    Sums all = {-INFINITY, 0.f, 0.f};
+    if (tid < segments) {
+      all.m = __uint_as_float(remote_word(&part.m, tid));
+      all.s = __uint_as_float(remote_word(&part.s, tid));
+      all.t = __uint_as_float(remote_word(&part.t, tid));
+    }
+    if (TOP) {
+      Key k = 0;
+      for (int i = warp; i < segments; i += kWarps) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&part_keys[lane]);
+        k = merge_keys(k, static_cast<Key>(remote_word(w + 1, i)) << 32 | remote_word(w, i));
+      }
+      lists[0][warp][lane] = k;
+    }
+    all = block_join(all);  // (the lists are complete behind its barrier)
+    if (tid == 0) write_row(o, r, all, x, vocab);
+    if (TOP && warp == 0) {
+      mine = merge_lists(lists[0]);
+      if (lane < top) write_top(o, r, top, all, mine);
+    }
   }
+  cluster_sync();  // no block leaves while its shared memory is read
 }
 
-// One block per row: joins the segments' sums and candidates.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) token_logprobs_join_kernel(const T* __restrict__ logits, int vocab, int64_t ld,
-                                                                      int segments, int top, Outs o,
-                                                                      const Sums* __restrict__ parts,
-                                                                      const Key* __restrict__ part_keys) {
-  __shared__ Key lists[kWarps][32];
-  pdl_enter();
-  const int64_t r = blockIdx.x;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Sums a = {-INFINITY, 0.f, 0.f};
-  if (threadIdx.x < segments) a = parts[r * segments + threadIdx.x];
-  Key mine = 0;
-  if (top > 0) {
-    for (int i = warp; i < segments; i += kWarps)
-      mine = merge_keys(mine, lane < top ? part_keys[(r * segments + i) * top + lane] : 0);
-    lists[warp][lane] = mine;
-  }
-  a = block_join(a);  // (the lists are complete behind its barrier)
-  if (threadIdx.x == 0) write_row(o, r, a, logits + r * ld, vocab);
-  if (warp == 0 && top > 0) {
-    mine = merge_lists(lists);
-    if (lane < top) write_top(o, r, top, a, mine);
-  }
-}
-
-// Segments a row is split in: enough blocks to fill the GPU once, each with at least 4096 logits
-// (less work than that is shorter than joining it). Splitting further, to even out the last wave,
-// costs more in candidates than it saves: 3000 x 131072 bf16, top 5: 172 us whole, 197 in halves.
+// Segments a row is split in (a power of two, up to a cluster's blocks): enough blocks to fill the
+// GPU once, each with at least 4096 logits (less work than that is shorter than joining it).
+// Splitting further, to even out the last wave, costs more in candidates than it saves: 3000 x
+// 131072 bf16, top 5: 172 us whole, 197 in halves.
 int logprob_segments(int64_t rows, int64_t vocab, int num_sms) {
   const int64_t slots = static_cast<int64_t>(num_sms) * (1024 / kThreads);
   const int64_t want = std::min((slots + rows - 1) / rows, vocab / 4096);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, kMaxSegments)));
+  int n = 1;
+  while (2 * n <= want && n < kMaxSegments) n *= 2;
+  return n;
 }
 
 template <typename T>
-cudaError_t launch_t(const T* x, int64_t rows, int vocab, int64_t ld, int top, const Outs& o, void* ws, int segments,
+cudaError_t launch_t(const T* x, int64_t rows, int vocab, int64_t ld, int top, const Outs& o, int segments,
                      cudaStream_t stream) {
-  Key* keys = static_cast<Key*>(ws);
-  Sums* parts = segments > 1 ? reinterpret_cast<Sums*>(keys + rows * segments * top) : nullptr;
-  const dim3 grid(static_cast<unsigned>(rows * segments));
   auto go = [&](auto kernel) {
     constexpr size_t smem = static_cast<size_t>(kStages) * kChunk * 16;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess && segments > 8)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, grid, dim3(kThreads), smem, stream, x, vocab, ld, segments, top, o, parts, keys);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * segments));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(segments);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = segments > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, x, vocab, ld, segments, top, o);
   };
   if (segments == 1)
     return top > 0 ? go(token_logprobs_kernel<T, true, true>) : go(token_logprobs_kernel<T, false, true>);
-  const cudaError_t e = top > 0 ? go(token_logprobs_kernel<T, true, false>) : go(token_logprobs_kernel<T, false, false>);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(token_logprobs_join_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0, stream, x, vocab,
-                    ld, segments, top, o, static_cast<const Sums*>(parts), static_cast<const Key*>(keys));
+  return top > 0 ? go(token_logprobs_kernel<T, true, false>) : go(token_logprobs_kernel<T, false, false>);
 }
 
 }  // namespace
 
-size_t token_logprobs_ws_bytes(int64_t rows, int64_t vocab, int64_t top, int num_sms) {
-  const int segments = logprob_segments(rows, vocab, num_sms);
-  return segments == 1 ? 0 : static_cast<size_t>(rows) * segments * (sizeof(Sums) + static_cast<size_t>(top) * 8);
-}
-
 cudaError_t launch_token_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
                                   const int64_t* tokens, int64_t top, float* logprob, float* entropy, int64_t* top_ids,
-                                  float* top_lp, void* ws, int num_sms, unsigned* err, cudaStream_t stream) {
+                                  float* top_lp, int num_sms, unsigned* err, cudaStream_t stream) {
   const Outs o{tokens, logprob, entropy, top_ids, top_lp, err};
   const int segments = logprob_segments(rows, vocab, num_sms), v = static_cast<int>(vocab), k = static_cast<int>(top);
-  if (dtype == 0) return launch_t(static_cast<const __nv_bfloat16*>(logits), rows, v, ld, k, o, ws, segments, stream);
-  if (dtype == 1) return launch_t(static_cast<const __half*>(logits), rows, v, ld, k, o, ws, segments, stream);
-  return launch_t(static_cast<const float*>(logits), rows, v, ld, k, o, ws, segments, stream);
+  if (dtype == 0) return launch_t(static_cast<const __nv_bfloat16*>(logits), rows, v, ld, k, o, segments, stream);
+  if (dtype == 1) return launch_t(static_cast<const __half*>(logits), rows, v, ld, k, o, segments, stream);
+  return launch_t(static_cast<const float*>(logits), rows, v, ld, k, o, segments, stream);
 }
 
 }  // namespace ttq

@@ -761,14 +761,15 @@ ttq_status ttq_attention_plan(const int32_t* q_start, const int32_t* kv_len, con
   const ttq::PagedShape s{seqs, tokens, max_new, heads, kv_heads, head_dim};
   ttq_status st = check_paged(s);
   if (st != TTQ_OK) return st;
+  DeviceInfo* di = nullptr;
+  const ttq_status dst = device_info(&di);
+  const size_t need = ttq::attention_plan_bytes(s, dst == TTQ_OK ? di->num_sms : 148);
   if (!grid_fits(s)) return TTQ_ERR_TOO_LARGE;
   if (window < 0 || window > (int64_t(1) << 30)) return TTQ_ERR_INVALID_ARG;
-  if (!plan || plan_bytes < ttq::attention_plan_bytes(s, sms_or_default())) return TTQ_ERR_WORKSPACE;
+  if (!plan || plan_bytes < need) return TTQ_ERR_WORKSPACE;
   if (!aligned4(q_start) || !aligned4(kv_len) || (prefix && !aligned4(prefix)) || !aligned16(plan))
     return TTQ_ERR_MISALIGNED;
-  DeviceInfo* di = nullptr;
-  st = device_info(&di);
-  if (st != TTQ_OK) return st;
+  if (dst != TTQ_OK) return dst;
   return cuda_status(ttq::launch_attention_plan(q_start, kv_len, prefix, window, s, plan, di->num_sms, di->err_word,
                                                 stream));
 }
@@ -789,13 +790,13 @@ ttq_status ttq_paged_attention(const void* q_bf16, int64_t ld_q, int64_t seqs, i
   if (ld_q < heads * head_dim || ld_q > (int64_t(1) << 30)) return TTQ_ERR_INVALID_ARG;
   if (!std::isfinite(softcap) || (softcap != 0.f && !(softcap >= 1e-30f))) return TTQ_ERR_INVALID_ARG;
   if (!grid_fits(s)) return TTQ_ERR_TOO_LARGE;
-  if (!plan || plan_bytes < ttq::attention_plan_bytes(s, sms_or_default())) return TTQ_ERR_WORKSPACE;
+  DeviceInfo* di = nullptr;
+  const ttq_status dst = device_info(&di);
+  if (!plan || plan_bytes < ttq::attention_plan_bytes(s, dst == TTQ_OK ? di->num_sms : 148)) return TTQ_ERR_WORKSPACE;
   if (!aligned16(q_bf16) || ld_q % 8 != 0 || !aligned16(out_bf16) || !aligned16(plan) ||
       (slopes && !aligned4(slopes)))
     return TTQ_ERR_MISALIGNED;
-  DeviceInfo* di = nullptr;
-  st = device_info(&di);
-  if (st != TTQ_OK) return st;
+  if (dst != TTQ_OK) return dst;
   return cuda_status(ttq::launch_paged_attention(q_bf16, ld_q, s, p, softcap, slopes, out_bf16, plan, di->num_sms,
                                                  dev_err(di), stream));
 }
@@ -866,17 +867,9 @@ ttq_status check_logprobs(int64_t rows, int64_t vocab, int64_t top) {
 }
 }  // namespace
 
-ttq_status ttq_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int64_t top, size_t* bytes) {
-  if (!bytes) return TTQ_ERR_INVALID_ARG;
-  const ttq_status st = check_logprobs(rows, vocab, top);
-  if (st != TTQ_OK) return st;
-  *bytes = round256(ttq::token_logprobs_ws_bytes(rows, vocab, top, sms_or_default()));
-  return TTQ_OK;
-}
-
 ttq_status ttq_token_logprobs(const void* logits, ttq_dtype dtype, int64_t rows, int64_t vocab, int64_t ld,
                               const int64_t* tokens, int64_t top, float* logprob, float* entropy, int64_t* top_ids,
-                              float* top_logprobs, void* ws, size_t ws_bytes, cudaStream_t stream) {
+                              float* top_logprobs, cudaStream_t stream) {
   if (!logits || !tokens || !logprob || !entropy) return TTQ_ERR_INVALID_ARG;
   if (dtype != TTQ_BF16 && dtype != TTQ_FP16 && dtype != TTQ_FP32) return TTQ_ERR_UNSUPPORTED;
   ttq_status st = check_logprobs(rows, vocab, top);
@@ -884,18 +877,15 @@ ttq_status ttq_token_logprobs(const void* logits, ttq_dtype dtype, int64_t rows,
   if (ld < vocab || (top > 0) != (top_ids != nullptr) || (top > 0) != (top_logprobs != nullptr) ||
       logprob == entropy)
     return TTQ_ERR_INVALID_ARG;
-  const size_t need = ttq::token_logprobs_ws_bytes(rows, vocab, top, sms_or_default());
-  if (need > 0 && (!ws || ws_bytes < need)) return TTQ_ERR_WORKSPACE;
   const uintptr_t elem = dtype == TTQ_FP32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(logits) % elem != 0 || !aligned8(tokens) || !aligned4(logprob) ||
-      !aligned4(entropy) || (top_ids && !aligned8(top_ids)) || (top_logprobs && !aligned4(top_logprobs)) ||
-      (ws && !aligned16(ws)))
+      !aligned4(entropy) || (top_ids && !aligned8(top_ids)) || (top_logprobs && !aligned4(top_logprobs)))
     return TTQ_ERR_MISALIGNED;
   DeviceInfo* di = nullptr;
   st = device_info(&di);
   if (st != TTQ_OK) return st;
   return cuda_status(ttq::launch_token_logprobs(logits, static_cast<int>(dtype), rows, vocab, ld, tokens, top, logprob,
-                                                entropy, top_ids, top_logprobs, ws, di->num_sms, di->err_word,
+                                                entropy, top_ids, top_logprobs, di->num_sms, di->err_word,
                                                 stream));
 }
 

@@ -289,9 +289,8 @@ cudaError_t launch_remap_pages(const int32_t* table, int64_t entries, const int3
 // ---------------------------------------------------------------- token log probabilities (logprobs.cu)
 
 // dtype: 0 bf16, 1 fp16, 2 fp32; top <= 32.
-size_t token_logprobs_ws_bytes(int64_t rows, int64_t vocab, int64_t top, int num_sms);
 cudaError_t launch_token_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
                                   const int64_t* tokens, int64_t top, float* logprob, float* entropy, int64_t* top_ids,
-                                  float* top_lp, void* ws, int num_sms, unsigned* err, cudaStream_t stream);
+                                  float* top_lp, int num_sms, unsigned* err, cudaStream_t stream);
 
 }  // namespace ttq

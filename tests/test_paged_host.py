@@ -118,22 +118,16 @@ def test_page_copy_and_remap_errors(lib):
 
 
 def test_logprob_errors(lib):
-    n = ctypes.c_size_t(0)
-    assert lib.ttq_token_logprobs_workspace_size(8, 1000, 5, ctypes.byref(n)) == OK
-    assert lib.ttq_token_logprobs_workspace_size(8, 1000, 5, None) == INVALID
-    assert lib.ttq_token_logprobs_workspace_size(8, 1000, 33, ctypes.byref(n)) == UNSUPPORTED
-    assert lib.ttq_token_logprobs_workspace_size(8, 4, 5, ctypes.byref(n)) == INVALID
-    assert lib.ttq_token_logprobs_workspace_size(8, (1 << 20) + 1, 5, ctypes.byref(n)) == INVALID
-
-    def lp(x=A, dt=0, rows=8, vocab=1000, ld=1000, tok=B, top=5, a=C, e=Q, ids=O, tl=W, ws=7 << 20, wsb=1 << 40):
-        return lib.ttq_token_logprobs(P(x), dt, rows, vocab, ld, P(tok), top, P(a), P(e), P(ids), P(tl), P(ws), wsb, None)
+    def lp(x=A, dt=0, rows=8, vocab=1000, ld=1000, tok=B, top=5, a=C, e=Q, ids=O, tl=W):
+        return lib.ttq_token_logprobs(P(x), dt, rows, vocab, ld, P(tok), top, P(a), P(e), P(ids), P(tl), None)
 
     assert lp(x=0) == INVALID and lp(tok=0) == INVALID and lp(a=0) == INVALID and lp(a=Q) == INVALID
     assert lp(dt=3) == UNSUPPORTED and lp(top=33) == UNSUPPORTED
+    assert lp(vocab=4) == INVALID and lp(vocab=(1 << 20) + 1, ld=1 << 21) == INVALID
     assert lp(rows=0) == INVALID and lp(vocab=0) == INVALID and lp(ld=999) == INVALID and lp(top=-1) == INVALID
     assert lp(ids=0) == INVALID and lp(tl=0) == INVALID and lp(top=0) == INVALID
     assert lp(x=A + 1) == MISALIGNED and lp(x=A + 2, dt=2) == MISALIGNED
-    assert lp(tok=B + 4) == MISALIGNED and lp(tl=W + 2) == MISALIGNED and lp(ws=(7 << 20) + 8) in (MISALIGNED, -5)
+    assert lp(tok=B + 4) == MISALIGNED and lp(tl=W + 2) == MISALIGNED
 
 
 def test_binding_refuses_wrong_tensors(lib):
