@@ -7,16 +7,20 @@
 //
 // The alternatives come out of the same pass. A logit's key is (order of its value, lowest index
 // first) in 64 bits, so no two are equal. Every warp keeps its best keys sorted, one a lane, and
-// inserts a key with two shuffles; only keys above a threshold get that far: the top-th best key
-// of the block so far. It starts from the lanes' best keys of the first chunk, sorted and merged
-// over the block, and is renewed after 2, 4, 8, ... chunks, when the warps hand their lists to the
-// first one (a merge of two sorted lists of 32 is six shuffles), so that about 5 `top` keys a row
-// are ever inserted. A chunk whose maximum is below the threshold costs one comparison a thread.
+// inserts a key with two shuffles; only keys above a threshold get that far, one that at least `top`
+// of the block's keys reach. It starts as the top-th of the threads' best keys of the first chunk
+// (sorted and merged over the block); later it is the lowest of the four warps' keys of rank
+// ceil(top / 4), which needs no meeting of the warps (merging the lists after 2, 4, 8, ... chunks
+// instead is a sharper threshold and fewer insertions, but 172 us against 167). A chunk whose maximum
+// is below the threshold costs one comparison a thread. About 10 `top` keys a row are inserted at
+// top = 5, 6 `top` at 20.
 //
-// Memory bound: one read of the logits. Few rows are split over the blocks of a cluster (segments),
-// whose first block reads the others' sums and candidates from their shared memory.
-#include <algorithm>
-#include <cmath>
+// Memory bound by its bytes (one read of the logits), but with 16-bit logits the exponentials alone
+// are 70% of that time (16 a cycle and SM), so sums and candidates show: 3000 x 131072 bf16 takes
+// 140 us without alternatives (5.6 TB/s), 167 with five (4.7 TB/s), 197 with twenty; 1500 x 131072
+// fp32 139 us with five (5.6 TB/s). Few rows are split over the blocks of a cluster (segments), whose
+// first block reads the others' sums and candidates from their shared memory: 8 x 50257 fp32 takes
+// 6.4 us without alternatives, 14.5 with twenty, whose sorts and insertions are a chain of shuffles.
 #include <type_traits>
 
 #include "attention_common.cuh"
@@ -30,7 +34,6 @@ constexpr int kVecs = 4;         // 16-byte vectors a thread takes per chunk
 constexpr int kStages = 3;       // chunks in flight, the one at work included
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = kVecs * kThreads;  // vectors of a chunk
-constexpr int kMaxTop = 32;      // one key a lane
 constexpr int kMaxSegments = 16;  // blocks of a cluster
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -228,9 +231,10 @@ template <typename T, bool TOP, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     token_logprobs_kernel(const T* __restrict__ logits, int vocab, int64_t ld, int segments, int top, Outs o) {
   constexpr int N = Vec<T>::N;
-  __shared__ Key lists[2][kWarps][32];  // the warps' lists, by turns
-  extern __shared__ uint4 ring[];       // [kStages][kVecs][kThreads]
-  __shared__ Key tau_sh;                // a key that at least `top` of the block's reach
+  extern __shared__ uint4 ring[];  // [kStages][kVecs][kThreads]
+  __shared__ Key lists[2][kWarps][32];       // the warps' lists after the first and the last chunk
+  __shared__ volatile Key share_sh[kWarps];  // the warps' keys of rank `share`
+  __shared__ volatile Key tau_sh;            // a key that at least `top` of the block's reach
   pdl_enter();
   const int tid = threadIdx.x;
   const int64_t r = ONE ? blockIdx.x : blockIdx.x / segments;
@@ -265,19 +269,20 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   Sums a = {-INFINITY, 0.f, 0.f};
   Key mine = 0;   // the warp's key of rank `lane`
   Key floor = 0;  // keys at or below it are not among the best
-  int turn = 0;
-  // every warp's list to the first, which publishes the threshold
-  auto gather = [&]() {
-    lists[turn][warp][lane] = mine;
-    __syncthreads();
-    if (warp == 0) {
-      mine = merge_lists(lists[turn]);
-      if (lane == top - 1) *const_cast<volatile Key*>(&tau_sh) = mine;
-    } else {
-      mine = 0;
-    }
-    turn ^= 1;
+  float fx = 0.f;  // the logit of `floor`
+  // The threshold after a change to the warp's list: its own top-th key, or the lowest of the warps'
+  // keys of rank `share` (as many keys as warps x (share + 1) reach that one). The other warps' keys
+  // may be older ones, which are lower.
+  const int share = (top + kWarps - 1) / kWarps - 1;
+  auto renew = [&]() {
+    Key t = share_sh[0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) t = min(t, share_sh[i]);
+    floor = __shfl_sync(0xffffffffu, max(floor, t), 0);
+    if (lane == 0 && floor > tau_sh) tau_sh = floor;
+    fx = key_value(static_cast<unsigned>(floor >> 32));
   };
+  if (TOP && tid == 0) tau_sh = 0;
   const int chunks = (v1 - v0 + kChunk - 1) / kChunk;
   auto fetch_chunk = [&](int i) {
     if (i < chunks) {
@@ -292,10 +297,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 #pragma unroll 1
   for (int chunk = 0; chunk < chunks; ++chunk) {
     const int c = v0 + chunk * kChunk;
+    const uint4* here = ring + (chunk % kStages) * kVecs * kThreads;
     if (TOP) __syncwarp();  // the warp is done with the chunk whose place is filled next
     fetch_chunk(chunk + kStages - 1);
     cp_async_wait<kStages - 1>();
-    const uint4* here = ring + (chunk % kStages) * kVecs * kThreads;
     uint4 w[kVecs];
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) w[u] = here[u * kThreads + tid];
@@ -319,60 +324,67 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     const float2 s1 = unpack2(s2), t1 = unpack2(t2);
     a.s += s1.x + s1.y;
     a.t += t1.x + t1.y;
-    if (TOP) {
-      Key best = 0;
-      if (chunk == 0) {
-        // the lane's best key (the first of equal logits)
-        int at = 0;
+    if (!TOP) continue;
+    Key best = 0;  // of the first chunk: the lane's best key (the first of equal logits)
+    if (chunk == 0) {
+      int at = 0;
 #pragma unroll
-        for (int u = kVecs - 1; u >= 0; --u)
+      for (int u = kVecs - 1; u >= 0; --u)
 #pragma unroll
-          for (int i = N / 2 - 1; i >= 0; --i) {
-            const float2 xx = Vec<T>::pair(w[u], i);
-            if (xx.y == bm) at = u * kThreads * N + 2 * i + 1;
-            if (xx.x == bm) at = u * kThreads * N + 2 * i;
-          }
-        if (bm > -INFINITY) best = make_key(bm, (c + tid) * N - head + at);
-        mine = sort_keys(best);
-        gather();
-        __syncthreads();
-      }
-      floor = max(floor, *const_cast<volatile Key*>(&tau_sh));
-      const float fx = key_value(static_cast<unsigned>(floor >> 32));
-      unsigned lanes = __ballot_sync(0xffffffffu, !(bm < fx));
-      if (lanes) {
-        // a lane with something above the threshold has its logits looked at by the whole warp, one
-        // a lane, from shared memory (rolled code: unrolled over the registers it costs more in
-        // instruction fetches than it does in work)
-        __syncwarp();  // the other lanes' logits have landed too
+        for (int i = N / 2 - 1; i >= 0; --i) {
+          const float2 xx = Vec<T>::pair(w[u], i);
+          if (xx.y == bm) at = u * kThreads * N + 2 * i + 1;
+          if (xx.x == bm) at = u * kThreads * N + 2 * i;
+        }
+      if (bm > -INFINITY) best = make_key(bm, (c + tid) * N - head + at);
+      mine = sort_keys(best);
+      lists[0][warp][lane] = mine;
+      if (lane == share) share_sh[warp] = mine;
+      __syncthreads();
+      floor = __shfl_sync(0xffffffffu, merge_lists(lists[0]), top - 1);
+      if (tid == 0) tau_sh = floor;
+      fx = key_value(static_cast<unsigned>(floor >> 32));
+    } else if (tau_sh > floor) {
+      floor = tau_sh;
+      fx = key_value(static_cast<unsigned>(floor >> 32));
+    }
+    unsigned lanes = __ballot_sync(0xffffffffu, !(bm < fx));
+    if (lanes) {
+      floor = __shfl_sync(0xffffffffu, floor, 0);  // (lanes may have read different thresholds)
+      // a lane with something above the threshold has its logits looked at by the whole warp, one
+      // a lane, from shared memory (rolled code: unrolled over the registers it costs more in
+      // instruction fetches than it does in work)
+      __syncwarp();  // the other lanes' logits have landed too
 #pragma unroll 1
-        while (lanes) {
-          const int src = __ffs(lanes) - 1;
-          lanes &= lanes - 1;
-          const int v = c + lane / N * kThreads + warp * 32 + src, k = v * N + lane % N - head;
-          Key key = 0;
-          if (lane < kVecs * N && v < v1 && k >= 0 && k < vocab)
-            key = make_key(to_float(reinterpret_cast<const T*>(here + lane / N * kThreads + warp * 32 + src)[lane % N]), k);
-          const Key known = __shfl_sync(0xffffffffu, best, src);
-          unsigned votes = __ballot_sync(0xffffffffu, key > floor && key != known);
+      while (lanes) {
+        const int src = __ffs(lanes) - 1;
+        lanes &= lanes - 1;
+        const int v = c + lane / N * kThreads + warp * 32 + src, k = v * N + lane % N - head;
+        Key key = 0;
+        if (lane < kVecs * N && v < v1 && k >= 0 && k < vocab)
+          key = make_key(to_float(reinterpret_cast<const T*>(here + lane / N * kThreads + warp * 32 + src)[lane % N]), k);
+        const Key known = __shfl_sync(0xffffffffu, best, src);
+        unsigned votes = __ballot_sync(0xffffffffu, key > floor && key != known);
 #pragma unroll 1
-          while (votes) {
-            const Key next = __shfl_sync(0xffffffffu, key, __ffs(votes) - 1);
-            votes &= votes - 1;
-            if (next <= floor) continue;  // (the same for the whole warp)
-            const int rank = __popc(__ballot_sync(0xffffffffu, mine > next));
-            const Key up = __shfl_up_sync(0xffffffffu, mine, 1);
-            if (lane == rank) mine = next;
-            if (lane > rank) mine = up;
-            floor = max(floor, __shfl_sync(0xffffffffu, mine, top - 1));
-          }
+        while (votes) {
+          const Key next = __shfl_sync(0xffffffffu, key, __ffs(votes) - 1);
+          votes &= votes - 1;
+          if (next <= floor) continue;  // (the same for the whole warp)
+          const int rank = __popc(__ballot_sync(0xffffffffu, mine > next));
+          const Key up = __shfl_up_sync(0xffffffffu, mine, 1);
+          if (lane == rank) mine = next;
+          if (lane > rank) mine = up;
+          floor = max(floor, __shfl_sync(0xffffffffu, mine, top - 1));
         }
       }
-      if (chunk > 0 && ((chunk + 1) & chunk) == 0 && chunk + 1 < chunks) gather();
+      if (lane == share) share_sh[warp] = mine;
+      __syncwarp();
+      renew();
     }
   }
-  if (TOP) gather();
-  a = block_join(a);
+  if (TOP) lists[1][warp][lane] = mine;
+  a = block_join(a);  // (the lists are complete behind its barrier)
+  if (TOP && warp == 0) mine = merge_lists(lists[1]);
   if (ONE) {
     if (tid == 0) write_row(o, r, a, x, vocab);
     if (TOP && tid < top) write_top(o, r, top, a, mine);
@@ -411,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 // Segments a row is split in (a power of two, up to a cluster's blocks): enough blocks to fill the
 // GPU once, each with at least 4096 logits (less work than that is shorter than joining it).
 // Splitting further, to even out the last wave, costs more in candidates than it saves: 3000 x
-// 131072 bf16, top 5: 172 us whole, 197 in halves.
+// 131072 bf16, top 5: 172 us whole, 197 in halves (measured with the threshold from merged lists).
 int logprob_segments(int64_t rows, int64_t vocab, int num_sms) {
   const int64_t slots = static_cast<int64_t>(num_sms) * (1024 / kThreads);
   const int64_t want = std::min((slots + rows - 1) / rows, vocab / 4096);
