@@ -119,6 +119,7 @@ class PagedCache:
         if len(seqs) == 0 or len(set(seqs)) != len(seqs) or len(seqs) != len(counts):
             raise ValueError("one count for each of at least one distinct sequences")
         need = 0
+        left = {}   # sequences that hold a shared last page, less those that copy it here
         for s, n in zip(seqs, counts):
             self._check(s)
             if n < 1:
@@ -127,10 +128,12 @@ class PagedCache:
                 raise ValueError(f"{self._length[s] + n} positions exceed {self.max_len}")
             held = len(self._pages[s])
             need += -(-(self._length[s] + n) // self.page_size) - held
-            if self._length[s] % self.page_size and self._held[self._pages[s][-1]] > 1:
-                need += 1
+            if self._length[s] % self.page_size:
+                last = self._pages[s][-1]
+                if left.setdefault(last, self._held[last]) > 1:
+                    left[last] -= 1
+                    need += 1
         if need > len(self._free):
-            # (an upper bound: the last holder of a shared page keeps it)
             raise RuntimeError(f"{need} pages are needed, {len(self._free)} are free")
         src, dst, where = [], [], []
         for s, n in zip(seqs, counts):
@@ -213,6 +216,17 @@ class PagedTTQDecoder(TTQDecoder):
                                 self.device)
         self.prompt = None
         self._plans = {}
+        self._needs, self._scratch = {}, None
+
+    def workspace(self, T: int):
+        """One scratch buffer for steps of any number of rows: it grows to the largest need."""
+        if T not in self._needs:
+            lins = [lin for L in self.layers for lin in L["lin"].values()]
+            lins += [] if self.lm_head is None else [self.lm_head]
+            self._needs[T] = max(ttq.workspace_size(T, lin.d, lin.d_out, lin.cfg) for lin in lins)
+        if self._scratch is None or self._scratch.numel() < self._needs[T]:
+            self._scratch = torch.empty(max(self._needs[T], 256), dtype=torch.uint8, device=self.device)
+        return self._scratch
 
     def _attention(self, li: int, qkv, T: int, prefill: bool):
         start, length, pages, plan = self._step
@@ -285,5 +299,6 @@ class PagedTTQDecoder(TTQDecoder):
         the head from these rows (a prompt's); later calls reuse its codes."""
         if self.lm_head is None:
             raise RuntimeError("the decoder has no output head")
-        logits = self.lm_head.prefill(hidden) if prefill else self.lm_head.decode(hidden)
+        ws = self.workspace(hidden.shape[0])
+        logits = self.lm_head.prefill(hidden, ws=ws) if prefill else self.lm_head.decode(hidden, ws=ws)
         return ttq.token_logprobs(logits, tokens, top)

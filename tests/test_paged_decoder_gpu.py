@@ -179,6 +179,33 @@ def test_cache_refusals_leave_it_as_it_was():
     assert c.page_list(a)[:2] == c.page_list(b)[:2] and c.page_list(a)[2] != c.page_list(b)[2]
 
 
+def test_branches_of_a_shared_last_page_take_what_is_there():
+    # three holders of a half full page step at once: two copies, the third keeps it; two pages are free
+    c = PagedCache(1, 5, 16, 1, 64, max_seqs=4, max_len=64)
+    a = c.new()
+    c.extend([a], [40])
+    b, d = c.fork(a), c.fork(a)
+    start, length, table = c.extend([a, b, d], [1, 2, 3])
+    assert c.free_pages == 0
+    assert sorted(c.page_list(s)[2] for s in (a, b, d)) == [2, 3, 4]
+    assert start.tolist() == [0, 1, 3, 6] and length.tolist() == [41, 42, 43]
+    assert [row[:3] for row in table.tolist()] == [c.page_list(s) for s in (a, b, d)]
+
+
+def test_steps_of_many_sizes_share_one_scratch_buffer():
+    dec = build(PagedTTQDecoder, max_len=256, pages=40, page_size=16, max_seqs=4)
+    dec.prefill(tokens(100, 3))
+    t = tokens(40, 4)
+    sizes = []
+    for n in (1, 33, 7):
+        f = dec.fork()[0]
+        dec.step([f], t[:n], [n])
+        dec.free(f)
+        sizes.append(dec.workspace(n).data_ptr())
+    assert len(set(sizes)) == 1 and not dec._ws
+    assert ttq.device_status() == 0
+
+
 def test_decoder_refusals():
     dec = build(PagedTTQDecoder, max_len=64, pages=8, page_size=16, max_seqs=2)
     x = tokens(10, 3)
