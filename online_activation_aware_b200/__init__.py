@@ -540,100 +540,32 @@ def silu_mul(gate_up, out=None, stream=None):
 # ------------------------------------------------------------------ paged cache, several sequences
 
 
-_torch = None
+_calls = None
 
 
-def _t():
-    """The torch module (imported at the first use)."""
-    global _torch
-    if _torch is None:
+def _native():
+    """The module that passes torch tensors to the paged entry points (``csrc/host_binding.cpp``)."""
+    global _calls
+    if _calls is None:
+        import importlib
+
         import torch
 
-        _torch = torch
-    return _torch
-
-
-def _types():
-    """(bf16, fp32, int32) of torch."""
-    torch = _t()
-    return torch.bfloat16, torch.float32, torch.int32
-
-
-class _Here:
-    """The context of a device that is current already."""
-
-    __slots__ = ()
-
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return None
-
-
-_HERE = _Here()
-
-
-def _device_of(*named) -> int:
-    """Index of the one CUDA device that all the given (name, tensor) pairs are on (None skipped)."""
-    index = None
-    for name, t in named:
-        if t is None:
-            continue
-        at = t.get_device()
-        if at != index:
-            if at < 0:
-                raise ValueError(f"{name} must be a CUDA tensor")
-            if index is not None:
-                raise ValueError(f"{name} is on cuda:{at}, the other tensors on cuda:{index}")
-            index = at
-    return index
-
-
-def _current(index: int):
-    """Context in which the device is current (the caller's comes back behind it)."""
-    cuda = _t().cuda
-    return _HERE if cuda.current_device() == index else cuda.device(index)
-
-
-def _fresh(stream, like, shape, dtype=None):
-    """A new tensor beside ``like``, from the memory of the stream that will use it."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    with _t().cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
-
-
-def _queue(stream, index: int) -> int:
-    """Handle of the given stream, or of the device's current one."""
-    return _t()._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-
-
-def _address(t, dtype, name):
-    """Address of a contiguous tensor of the given type (None -> NULL)."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _shape(t, name, dims):
-    """Raises unless t (None skipped) has the given sizes."""
-    if t is not None and tuple(t.shape) != dims:
-        raise ValueError(f"{name} must have shape {list(dims)}, got {list(t.shape)}")
-
-
-def _pool(k_pages, v_pages, page_table, seqs: int, kv_heads: int, head_dim: int):
-    shape = tuple(k_pages.shape)
-    if len(shape) != 4 or shape[2:] != (kv_heads, head_dim):
-        raise ValueError(f"k_pages must have shape [pages, page_size, {kv_heads}, {head_dim}], got {list(shape)}")
-    _shape(v_pages, "v_pages", shape)
-    if page_table.dim() != 2 or page_table.shape[0] != seqs:
-        raise ValueError(f"page_table must have shape [{seqs}, width], got {list(page_table.shape)}")
-    return shape[0], shape[1], page_table.shape[1]
+        lib = load_library()
+        try:
+            host = importlib.import_module(__name__ + "._host")
+        except ImportError as e:
+            raise RuntimeError(f"{__name__}._host is missing or does not load ({e}): build it with "
+                               "`python -m online_activation_aware_b200.build`") from e
+        if host.torch_version != torch.__version__:
+            raise RuntimeError(f"{__name__}._host was built for torch {host.torch_version}, this is "
+                               f"{torch.__version__}: build it again")
+        entries = (lib.ttq_attention_plan, lib.ttq_paged_attention, lib.ttq_qk_norm_rope_paged, lib.ttq_copy_pages,
+                   lib.ttq_remap_pages, lib.ttq_token_logprobs)
+        host.bind(tuple(ctypes.cast(f, ctypes.c_void_p).value for f in entries), _check,
+                  torch.OutOfMemoryError)
+        _calls = host
+    return _calls
 
 
 class AttentionPlan:
@@ -662,16 +594,7 @@ class AttentionPlan:
         """Plans a step: sequence b's new tokens are rows q_start[b] .. q_start[b+1] - 1, its
         cache holds kv_len[b] positions with them (int32 tensors). ``window`` > 0 limits every
         token to that many positions; the first prefix[b] positions stay visible to all."""
-        bf16, f32, i32 = _types()
-        _shape(q_start, "q_start", (self.seqs + 1,))
-        _shape(kv_len, "kv_len", (self.seqs,))
-        _shape(prefix, "prefix", (self.seqs,))
-        on = _device_of(("q_start", q_start), ("kv_len", kv_len), ("prefix", prefix), ("plan", self.buffer))
-        with _current(on):
-            _check("ttq_attention_plan", load_library().ttq_attention_plan(
-                _address(q_start, i32, "q_start"), _address(kv_len, i32, "kv_len"),
-                _address(prefix, i32, "prefix"), window, self.seqs, self.tokens, self.max_new, self.heads,
-                self.kv_heads, self.head_dim, self.buffer.data_ptr(), self.buffer.numel(), _queue(stream, on)))
+        _native().plan(self, q_start, kv_len, window, prefix, stream)
         return self
 
 
@@ -682,26 +605,7 @@ def paged_attention(q, plan: AttentionPlan, k_pages, v_pages, page_table, softca
     [num_pages, page_size, kv_heads, head_dim] bf16, page_table [seqs, width] int32. Scores are
     capped to softcap * tanh(s / softcap) when softcap > 0, then biased by slopes[h] * (k - pos).
     Returns out [tokens, heads * head_dim] bf16; rows past the last sequence are not written."""
-    bf16, f32, i32 = _types()
-    H, D, T = plan.heads, plan.head_dim, plan.tokens
-    pages, page_size, width = _pool(k_pages, v_pages, page_table, plan.seqs, plan.kv_heads, D)
-    _shape(slopes, "slopes", (H,))
-    _shape(out, "out", (T, H * D))
-    if q.dim() != 2 or q.shape[0] != T or q.shape[1] < H * D or q.stride(1) != 1:
-        raise ValueError(f"q must be {T} rows of at least {H * D} contiguous channels, got {list(q.shape)}")
-    if q.dtype != bf16:
-        raise TypeError(f"q must be {bf16}, got {q.dtype}")
-    on = _device_of(("q", q), ("k_pages", k_pages), ("v_pages", v_pages), ("page_table", page_table),
-                    ("slopes", slopes), ("out", out), ("plan", plan.buffer))
-    with _current(on):
-        if out is None:
-            out = _fresh(stream, q, (T, H * D))
-        _check("ttq_paged_attention", load_library().ttq_paged_attention(
-            q.data_ptr(), q.stride(0) if T > 1 else H * D, plan.seqs, T, plan.max_new, H, plan.kv_heads, D,
-            _address(k_pages, bf16, "k_pages"), _address(v_pages, bf16, "v_pages"), pages, page_size,
-            _address(page_table, i32, "page_table"), width, softcap, _address(slopes, f32, "slopes"),
-            _address(out, bf16, "out"), plan.buffer.data_ptr(), plan.buffer.numel(), _queue(stream, on)))
-    return out
+    return _native().attention(q, plan, k_pages, v_pages, page_table, softcap, slopes, out, stream)
 
 
 def qk_norm_rope_paged(qkv, heads: int, kv_heads: int, head_dim: int, q_norm, k_norm, eps: float, table, q_start,
@@ -710,30 +614,8 @@ def qk_norm_rope_paged(qkv, heads: int, kv_heads: int, head_dim: int, q_norm, k_
     written to their sequences' pages at positions kv_len[b] - n .. kv_len[b] - 1, and the
     normalised, rotated q heads to q [tokens, heads * head_dim], which is returned (qkv is only
     read; rows past the last sequence are not written)."""
-    bf16, f32, i32 = _types()
-    T = qkv.shape[0]
-    seqs = kv_len.shape[0]
-    _shape(qkv, "qkv", (T, (heads + 2 * kv_heads) * head_dim))
-    pages, page_size, width = _pool(k_pages, v_pages, page_table, seqs, kv_heads, head_dim)
-    _shape(q_start, "q_start", (seqs + 1,))
-    _shape(kv_len, "kv_len", (seqs,))
-    _shape(q_norm, "q_norm", (head_dim,))
-    _shape(k_norm, "k_norm", (head_dim,))
-    _shape(table, "table", (table.shape[0], head_dim // 2, 2))
-    _shape(q, "q", (T, heads * head_dim))
-    on = _device_of(("qkv", qkv), ("q_norm", q_norm), ("k_norm", k_norm), ("table", table), ("q_start", q_start),
-                    ("kv_len", kv_len), ("k_pages", k_pages), ("v_pages", v_pages), ("page_table", page_table),
-                    ("q", q))
-    with _current(on):
-        if q is None:
-            q = _fresh(stream, qkv, (T, heads * head_dim))
-        _check("ttq_qk_norm_rope_paged", load_library().ttq_qk_norm_rope_paged(
-            _address(qkv, bf16, "qkv"), seqs, T, heads, kv_heads, head_dim, _address(q_norm, bf16, "q_norm"),
-            _address(k_norm, bf16, "k_norm"), eps, _address(table, f32, "table"), table.shape[0],
-            _address(q_start, i32, "q_start"), _address(kv_len, i32, "kv_len"),
-            _address(k_pages, bf16, "k_pages"), _address(v_pages, bf16, "v_pages"), pages, page_size,
-            _address(page_table, i32, "page_table"), width, _address(q, bf16, "q"), _queue(stream, on)))
-    return q
+    return _native().write(qkv, heads, kv_heads, head_dim, q_norm, k_norm, eps, table, q_start, kv_len, k_pages, v_pages,
+                           page_table, q, stream)
 
 
 def copy_pages(k_pool, v_pool, src, dst, stream=None):
@@ -741,40 +623,13 @@ def copy_pages(k_pool, v_pool, src, dst, stream=None):
     [num_pages, page_size, kv_heads, head_dim] or [layers, num_pages, ...], of one type; src and
     dst int32 tensors on the pools' device. Every destination appears once and is no source of
     another pair."""
-    bf16, f32, i32 = _types()
-    shape = tuple(k_pool.shape)
-    if len(shape) not in (4, 5):
-        raise ValueError("pools are [num_pages, page_size, kv_heads, head_dim], with the layers ahead or without")
-    _shape(v_pool, "v_pool", shape)
-    if src.dim() != 1:
-        raise ValueError("src and dst are lists of pages")
-    _shape(dst, "dst", tuple(src.shape))
-    layers = shape[0] if len(shape) == 5 else 1
-    page_bytes = shape[-3] * shape[-2] * shape[-1] * k_pool.element_size()
-    on = _device_of(("k_pool", k_pool), ("v_pool", v_pool), ("src", src), ("dst", dst))
-    with _current(on):
-        if src.shape[0] == 0:
-            return
-        _check("ttq_copy_pages", load_library().ttq_copy_pages(
-            _address(k_pool, k_pool.dtype, "k_pool"), _address(v_pool, k_pool.dtype, "v_pool"), layers, shape[-4],
-            page_bytes, _address(src, i32, "src"), _address(dst, i32, "dst"), src.shape[0], _queue(stream, on)))
+    _native().copy(k_pool, v_pool, src, dst, stream)
 
 
 def remap_pages(table, mapping, out=None, stream=None):
     """Page tables after their pages moved: out = mapping[table] for entries that are pages,
     negative entries as they are (int32 tensors; ``out`` may be ``table``)."""
-    bf16, f32, i32 = _types()
-    if mapping.dim() != 1:
-        raise ValueError("mapping holds one entry a page")
-    _shape(out, "out", tuple(table.shape))
-    on = _device_of(("table", table), ("mapping", mapping), ("out", out))
-    with _current(on):
-        if out is None:
-            out = _fresh(stream, table, table.shape)
-        _check("ttq_remap_pages", load_library().ttq_remap_pages(
-            _address(table, i32, "table"), table.numel(), _address(mapping, i32, "mapping"), mapping.shape[0],
-            _address(out, i32, "out"), _queue(stream, on)))
-    return out
+    return _native().remap(table, mapping, out, stream)
 
 
 def token_logprobs(logits, tokens, top: int = 0, stream=None):
@@ -783,24 +638,4 @@ def token_logprobs(logits, tokens, top: int = 0, stream=None):
     a padding row, log probability 0). Returns dict(logprob [rows], entropy [rows]) and, with
     top > 0, top_ids (int64) and top_logprobs [rows, top]: the most likely tokens in falling
     order, equal logits by rising index."""
-    torch = _t()
-    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
-        raise ValueError("logits must be rows of contiguous logits")
-    rows, vocab = logits.shape
-    _shape(tokens, "tokens", (rows,))
-    kind = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(logits.dtype)
-    if kind is None:
-        raise TypeError(f"logits must be bf16, fp16 or fp32, got {logits.dtype}")
-    on = _device_of(("logits", logits), ("tokens", tokens))
-    with _current(on):
-        out = {"logprob": _fresh(stream, logits, rows, torch.float32),
-               "entropy": _fresh(stream, logits, rows, torch.float32)}
-        ids = lps = None
-        if top > 0:
-            ids = out["top_ids"] = _fresh(stream, logits, (rows, top), torch.int64)
-            lps = out["top_logprobs"] = _fresh(stream, logits, (rows, top), torch.float32)
-        _check("ttq_token_logprobs", load_library().ttq_token_logprobs(
-            logits.data_ptr(), kind, rows, vocab, logits.stride(0) if rows > 1 else vocab,
-            _address(tokens, torch.int64, "tokens"), top, out["logprob"].data_ptr(), out["entropy"].data_ptr(),
-            None if ids is None else ids.data_ptr(), None if lps is None else lps.data_ptr(), _queue(stream, on)))
-    return out
+    return _native().logprobs(logits, tokens, top, stream)

@@ -1,8 +1,10 @@
 """Builds libttq.so (the C-ABI library of the TTQ hot path) in-tree with nvcc for
-sm_100a. Usage: ``python -m online_activation_aware_b200.build`` (or call ``build()``).
+sm_100a, and ``_host.so`` (the Python module that passes torch tensors to its paged entry
+points) with the host compiler. Usage: ``python -m online_activation_aware_b200.build`` (or
+call ``build()``).
 
-Object files go to ``_build/`` at the repository root; the shared library is written
-next to this file so that the snapshot of the repository carries it."""
+Object files go to ``_build/`` at the repository root; the shared libraries are written
+next to this file so that the snapshot of the repository carries them."""
 
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libttq.so")
+HOST_SRC = os.path.join(CSRC, "host_binding.cpp")
+HOST = os.path.join(PKG, "_host.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -41,8 +46,39 @@ def _deps_mtime():
     return max(os.path.getmtime(p) for p in paths)
 
 
+def build_host(verbose: bool = False, force: bool = False) -> str:
+    """Compiles the Python module of the paged entry points against the installed torch."""
+    import torch
+
+    stamp = os.path.join(BUILD, "host.torch")
+    built_for = open(stamp).read() if os.path.exists(stamp) else None
+    newest = max(os.path.getmtime(HOST_SRC), os.path.getmtime(os.path.join(INCLUDE, "ttq.h")))
+    if not force and built_for == torch.__version__ and os.path.exists(HOST) and os.path.getmtime(HOST) >= newest:
+        return HOST
+    os.makedirs(BUILD, exist_ok=True)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    torch_dir = os.path.dirname(torch.__file__)
+    dirs = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(cuda, "include"),
+            os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include")]
+    tmp = HOST + ".tmp"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
+           f"-DTTQ_TORCH_VERSION=\"{torch.__version__}\"", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *(f"-I{d}" for d in dirs), HOST_SRC, "-o", tmp, "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd))
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the host compiler failed on {HOST_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, HOST)
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
+    return HOST
+
+
 def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
-    """Compiles every .cu under csrc/ and links libttq.so. Returns the library path."""
+    """Compiles every .cu under csrc/ and links libttq.so, and the host module beside it. Returns
+    the library path."""
+    build_host(verbose, force)
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
         return LIB
     nvcc = _nvcc()

@@ -46,7 +46,8 @@ constexpr int kWriteThreads = 128;
 // rotation needs no exchange. Memory bound in bytes (qkv is read once, q, k and v written once), but
 // the arithmetic of a norm and a rotation is near it: two channels an instruction, few lanes a slot
 // (the norm's root and reciprocal are the same work however many lanes share them), and the
-// token's angles (64 bytes a lane) kept in registers for the group's slots.
+// token's angles (64 bytes a lane) kept in registers for the group's slots. Nine prompts of 400 - 1900
+// tokens, 32 + 8 + 8 heads of 128 (169 MB): 36 us, 4.6 TB/s; 64 single tokens 2.9 us.
 template <int LN, int P>
 __global__ void __launch_bounds__(kWriteThreads) qk_norm_rope_paged_kernel(
     const __nv_bfloat16* __restrict__ qkv, int seqs, int tokens, int heads, int kv_heads,
@@ -146,7 +147,8 @@ __global__ void __launch_bounds__(kWriteThreads) qk_norm_rope_paged_kernel(
 
 // Copies: memory bound, every moved page read and written once. A block moves 16 KB, four loads a
 // thread ahead of its four stores; a page is as many blocks as it takes, so that a fork of a few
-// pages fills the GPU as well.
+// pages fills the GPU as well. 1200 pages of 64 KB in 6 layers, K and V: 1.9 GB moved in 286 us, 6.6
+// TB/s, the rate of a plain copy; 7 pages of 32 KB in 36 layers: 4.3 us.
 constexpr int kCopyVecs = 4;
 
 __global__ void __launch_bounds__(256) copy_pages_kernel(uint4* k, uint4* v, int64_t num_pages, int64_t page_vecs,
@@ -203,7 +205,8 @@ cudaError_t launch_qk_norm_rope_paged(const void* qkv, const PagedShape& s, cons
   int page_log2 = 0;
   while ((int64_t(1) << page_log2) < p.page_size) ++page_log2;
   // Four slots a group once that still gives every SM 32 warps; below, one slot a group (a decode
-  // step is latency: the fewer in a row the better).
+  // step is latency: the fewer in a row the better). 32 + 8 + 8 heads of 128, four slots and one:
+  // 64 tokens 10.0 and 8.2 us, 2048 tokens 18.5 and 20.2, 10000 tokens 51 and 61 (L2 flushed).
   const bool wide = s.tokens * slots * ln >= int64_t(num_sms) * 32 * 32 * 4;
   const int64_t per = wide ? 4 : 1;
   const int64_t threads = s.tokens * ((slots + per - 1) / per) * ln;

@@ -83,7 +83,9 @@ PlanLayout plan_layout(const PagedShape& s, int num_sms) {
   PlanLayout l = {};
   const int64_t G = s.heads / s.kv_heads;
   // Few rows a sequence go to mma.sync, whose 16-row blocks leave the least work to rows that
-  // are not there; more rows to tcgen05.
+  // are not there; more rows to tcgen05. (64 sequences of 4096 positions, 8 key/value heads of 128:
+  // 1, 8, 16 rows take 186, 188, 193 us on mma.sync and 227, 229, 232 on tcgen05; 4 sequences 29, 31,
+  // 35 and 49, 43, 43.)
   const bool few = s.max_new * G <= kFewRows;
   l.rows = few ? kFewRows : 2 * kHalfRows;
   l.tq = static_cast<int>(few ? kFewRows / G : 2 * (kHalfRows / G));
@@ -136,10 +138,11 @@ __device__ __forceinline__ TileKeys tile_keys(int p0, int ntok, int pre, int win
 }
 
 // Units of work of a tile with that many key tiles: starting and finishing one costs about as much
-// as two key tiles of few rows, or eight of many.
+// as two key tiles of few rows, or eight of many. (Not priced, 24 ragged sequences of 1 - 300 new
+// tokens with masks take 74 us instead of 66, six of 90 - 700 113 instead of 109.)
 __device__ __forceinline__ int tile_cost(int total, bool few) { return total + (few ? 2 : 8); }
 // A cut this near to the end of a tile moves there: writing and joining partial results costs as
-// much again.
+// much again. (Without: 68 and 111 us for those two.)
 __device__ __forceinline__ int cut_slack(bool few) { return few ? 2 : 6; }
 
 __device__ __forceinline__ uint64_t warp_scan(uint64_t x) {
@@ -469,6 +472,12 @@ struct PageFeed {
 constexpr int kFewThreads = 160;   // 4 warps of products, 1 of copies
 constexpr int kFewMaxStages = 8;
 
+// Bound by memory: K and V of every sequence are read once, for G rows of 4 D flop a key, which the
+// mma.sync units do on the side (64 sequences of 300 - 9000 positions, 32 heads on 8: 731 MB in 124 us,
+// 5.9 TB/s; 3 of 60 - 131 thousand, 64 on 8: 1.03 GB in 166 us, 6.2 TB/s). Every resident block has an
+// equal share of the step's key tiles, so a long sequence is spread over the GPU and short ones share
+// a block.
+//
 // smem: a ring of stages (K and V of one key tile, in boxes of 64 channels), then the exchange of
 // the warps' results [4][row_cap][D]. Two CTAs share an SM; each takes as many stages as fit.
 template <int D>
@@ -839,11 +848,22 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
 
 // ---------------------------------------------------------------- many rows: tcgen05
 
+// Bound by the tensor cores: 4 D flop per row and visible key (4096 new tokens behind 12315, 40 heads on
+// 8: 1.2 PFLOP, 733 us at the measured burst rate; 1058 us here, 1.14 PFLOP/s, tensor pipe 53% and
+// special function units 40% active; back to back under the power cap 1260 us, where the cap's
+// rate would take 880). A block is 256 rows in two halves, so that a tile of keys in shared memory
+// serves both and one half's products run under the other's softmax (128 rows and two blocks an SM:
+// 1758 us; this with one place of scores a half: 1197).
+//
 // 11 warps: 0-3 and 4-7 the softmax of the two halves (128 rows each, a row a thread), 8 copies, 9
 // and 10 the products of a half each (one warp for both could not issue them fast enough: 2800
-// cycles a key tile, twice what they take). The scores of a half have two places in tensor memory, so that its next product
-// runs while its softmax works. (With one place of twice the keys, a half's softmax and its products
-// took turns: 46% of the tensor cores' cycles, where this form has xx%.)
+// cycles a key tile, twice what they take). The scores of a half have two places in tensor memory, so
+// that its next product runs while its softmax works; with O they take all 512 columns. That leaves
+// 64 keys a product, and Q K^T that narrow reads Q from shared memory (48 KB a product of 2^20
+// multiply-adds) faster than it multiplies: 483 cycles for what 128 keys do in 530, against 287 for
+// P V (64 keys, P in tensor memory). Places of 128 keys, one a half, were no faster (1063 - 1118 us:
+// softmax and products of a half take turns again), nor were 128 rows with two halves of keys
+// (1166), nor two threads a row in 16 softmax warps (1147).
 constexpr int kManyThreads = 352;
 constexpr float kRescaleSlack = 8.0f;          // log2 units a row maximum may rise before O is rescaled
 constexpr uint32_t kRowBox = kHalfRows * 128;  // a box of Q: 128 rows x 128 B

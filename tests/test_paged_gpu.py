@@ -549,3 +549,43 @@ def test_token_logprobs_captured():
         want = check_logprobs(x, tok, 5)
         for name in want:
             assert torch.equal(got[name], want[name])
+
+
+# ---------------------------------------------------------------- arguments
+
+
+def test_tensors_of_the_wrong_kind_are_refused():
+    H, Hkv, D, B, W, page = 8, 2, 64, 2, 3, 16
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device="cuda")
+    i = lambda *s: z(*s, dt=torch.int32)
+    plan = ttq.AttentionPlan(B, 4, H, Hkv, D, max_new=3)
+    qs, kl, pt = torch.tensor([0, 1, 4], dtype=torch.int32, device="cuda"), i(B) + 20, i(B, W)
+    k, v = z(4, page, Hkv, D), z(4, page, Hkv, D)
+    q = z(4, H * D)
+    plan.update(qs, kl)
+    att = lambda **o: ttq.paged_attention(**{**dict(q=q, plan=plan, k_pages=k, v_pages=v, page_table=pt), **o})
+    for wrong, kind in ((dict(q=q.half()), TypeError), (dict(q=q.cpu()), ValueError), (dict(q=z(3, H * D)), ValueError),
+                        (dict(q=z(4, H * D - 8)), ValueError), (dict(q=z(H * D, 4).t()), ValueError),
+                        (dict(k_pages=k.float()), TypeError), (dict(v_pages=z(5, page, Hkv, D)), ValueError),
+                        (dict(k_pages=z(4, page, D, Hkv).transpose(2, 3)), ValueError),
+                        (dict(page_table=pt.long()), TypeError), (dict(page_table=i(B + 1, W)), ValueError),
+                        (dict(page_table=i(W, B).t()), ValueError), (dict(slopes=z(H)), TypeError),
+                        (dict(slopes=z(H + 1, dt=torch.float32)), ValueError), (dict(out=z(4, H * D + 8)), ValueError),
+                        (dict(softcap=-1.0), ttq.TTQError), (dict(softcap="a"), TypeError), (dict(q=None), TypeError),
+                        (dict(k_pages=z(4, 24, Hkv, D), v_pages=z(4, 24, Hkv, D)), ttq.TTQError)):
+        with pytest.raises(kind):
+            att(**wrong)
+    for wrong, kind in ((dict(q_start=qs[:2]), ValueError), (dict(q_start=qs.long()), TypeError),
+                        (dict(kv_len=kl.cpu()), ValueError), (dict(prefix=i(B + 1)), ValueError),
+                        (dict(window=-1), ttq.TTQError), (dict(window=1.5), TypeError)):
+        with pytest.raises(kind):
+            plan.update(**{**dict(q_start=qs, kv_len=kl), **wrong})
+    with pytest.raises(ttq.TTQError):
+        ttq.token_logprobs(z(2, 10), torch.zeros(2, dtype=torch.int64, device="cuda"), top=11)
+    with pytest.raises(ttq.TTQError):
+        ttq.token_logprobs(z(2, 10), torch.zeros(2, dtype=torch.int64, device="cuda"), top=-1)
+    out = z(4, H * D) + 3
+    assert att(out=out) is out and torch.count_nonzero(out) == 0
+    table = i(B, W)
+    assert ttq.remap_pages(table, i(4) + 2, out=table) is table and bool((table == 2).all())
+    assert ttq.device_status() == 0

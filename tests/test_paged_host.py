@@ -150,3 +150,10 @@ def test_binding_refuses_wrong_tensors(lib):
         ttq.token_logprobs(z(3, 8, dt=torch.float64), torch.zeros(3, dtype=torch.int64))
     with pytest.raises(ttq.TTQError):
         ttq.AttentionPlan(2, 4, 30, 8, 128, device="cpu")
+    with pytest.raises(TypeError):
+        ttq.remap_pages([1, 2], i(4))                                         # no tensor
+    with pytest.raises(TypeError):
+        ttq.token_logprobs(z(3, 8), torch.zeros(3, dtype=torch.int64), top="five")
+    with pytest.raises(ValueError):
+        ttq.qk_norm_rope_paged(z(3, 4 * 64), 2, 1, 64, z(64), z(64), 1e-6, z(9, 32, 2, dt=torch.float32), i(2), i(1),
+                               z(4, 16, 1, 64), z(4, 16, 1, 64), i(1, 2))     # CPU tensors
