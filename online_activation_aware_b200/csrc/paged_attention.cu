@@ -117,6 +117,11 @@ PlanLayout plan_layout(const PagedShape& s, int num_sms) {
   return l;
 }
 
+// Units of work that joining one piece more costs (tiles of many rows: the joining block reads 64 KB a
+// piece and half alone; of few rows it is nothing). 30 new tokens behind 6000, 32 heads on 8: 40 us if
+// not priced, 34 us; 64 behind 2000, two sequences, 16 on 4: 33 and 29.
+constexpr float kJoinCost = 2.f;
+
 struct TileKeys {
   int total, nA, lo;
 };
@@ -184,8 +189,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
   __shared__ int2 tile_seq_sh[kPlanTiles];
   __shared__ uint64_t tile_at_sh[kPlanTiles];
   __shared__ int cta_first_sh[kPlanCtas];
+  __shared__ int longest;  // cost of the longest tile
   pdl_enter();
   const int tid = threadIdx.x;
+  const bool few = l.rows == kFewRows;
   PlanHeader* out = reinterpret_cast<PlanHeader*>(plan);
   int* cta_first = reinterpret_cast<int*>(plan + l.off_cta);
   Piece* pieces = reinterpret_cast<Piece*>(plan + l.off_pieces);
@@ -194,6 +201,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
   const bool small = l.max_tiles <= kPlanTiles;
   int2* tile_seq = small ? tile_seq_sh : reinterpret_cast<int2*>(plan + l.off_tile_seq);
   uint64_t* tile_at = small ? tile_at_sh : reinterpret_cast<uint64_t*>(plan + l.off_tile_at);
+  if (tid == 0) longest = 0;
   // lengths in range?
   bool bad = false;
   for (int b = tid; b < h.seqs; b += kPlanThreads) {
@@ -252,15 +260,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
     uint64_t cost = 0, tot;
     if (t < ntiles) {
       Piece p;
-      cost = static_cast<uint64_t>(tile_cost(tile_of(t, &p).total, l.rows == kFewRows)) * h.kv_heads;
+      const int units = tile_cost(tile_of(t, &p).total, few);
+      atomicMax(&longest, units);
+      cost = static_cast<uint64_t>(units) * h.kv_heads;
     }
     const uint64_t at = work + block_scan(cost, &tot, sh, turn);
     if (t < ntiles) tile_at[t] = at;
     work += tot;
   }
   __syncthreads();
-  // equal shares; a share shorter than a few key tiles is not worth its start
-  const uint64_t share = max(static_cast<uint64_t>(4), (work + l.ctas - 1) / l.ctas);
+  // equal shares, but no shorter than pays: with n pieces the longest tile takes longest / n + n joins,
+  // least at n = sqrt(longest / join)
+  const float least = few ? 2.f : fmaxf(4.f, sqrtf(kJoinCost * static_cast<float>(longest)));
+  const uint64_t share = max(static_cast<uint64_t>(least), (work + l.ctas - 1) / l.ctas);
   const float inv_share = 1.f / static_cast<float>(share);
   for (int c = tid; c < l.ctas; c += kPlanThreads) cta_first_sh[c] = 0x7fffffff;
   __syncthreads();
@@ -277,10 +289,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* __restric
       const int t = i / h.kv_heads;
       p.kvh = i - t * h.kv_heads;
       total = tile_of(t, &p).total;
-      cost = tile_cost(total, l.rows == kFewRows);
+      cost = tile_cost(total, few);
       a = tile_at[t] + static_cast<uint64_t>(p.kvh) * cost;
       // cuts up to `slack` inside the item move to its ends; those between cut it
-      const int slack = min(cut_slack(l.rows == kFewRows), cost / 2);
+      const int slack = min(cut_slack(few), cost / 2);
       c0 = divide(a + slack, share, inv_share);
       np = static_cast<int>(max(c0, divide(a + cost - slack - 1, share, inv_share)) - c0 + 1);
       v = static_cast<uint64_t>(np) << 32 | (np > 1 ? static_cast<uint64_t>(np) << 16 | 1u : 0u);
@@ -554,11 +566,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
   __syncthreads();
   pdl_enter();
   const PlanHeader hdr = *reinterpret_cast<const PlanHeader*>(a.plan);
+  const int2 range = cta_pieces(a, blockIdx.x);  // (loaded with the header: one trip to L2 less)
   if (!plan_ok(hdr, a.want)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err.word, kErrRange);
     return;
   }
-  const int2 range = cta_pieces(a, blockIdx.x);
   if (range.x >= range.y) return;
   const int G = a.G;
   int st = 0, ph = 0;  // stage of the ring and its turn
@@ -880,7 +892,11 @@ struct ManyBars {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
-  int last[2];                 // a half's piece is the last of its tile to be done
+  int joins[2];                // tiles that a half joins at the block's end
+  struct {
+    Split* split;
+    int slot0, pieces, tok0, ntok, kvh;
+  } join[2][2];
 };
 
 // smem: Q of both halves | ring of tiles K_0, K_1 V_0, K_2 V_1, ..., V_last, in 1024-byte aligned
@@ -1026,6 +1042,69 @@ __device__ __forceinline__ void load_o(uint32_t to, int cc, bool any, uint32_t (
   }
 }
 
+// A row of a split tile from the partial results of all its pieces, in their order. 32 channels of
+// three pieces at a time, all their loads in flight: the block that joins reads 64 KB a piece and half
+// alone, so it is bound by what one SM takes from L2 (30 new tokens behind 20000 in 18 pieces a
+// tile: 55 us, 64 with one piece in flight).
+template <int D>
+__device__ __forceinline__ void join_row(const float2* mls, const float4* parts, int np, __nv_bfloat16* out) {
+  constexpr int kRows = 2 * kHalfRows;  // of a partial result
+  float M = -FLT_MAX, Ls = 0.f;
+#pragma unroll 1
+  for (int n0 = 0; n0 < np; n0 += 8) {
+    float2 ml[8];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) ml[n] = n0 + n < np ? __ldcg(mls + (n0 + n) * kRows) : make_float2(-FLT_MAX, 0.f);
+    float top = M;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) top = fmaxf(top, ml[n].x);
+    Ls *= exp2_approx(M - top);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) Ls = fmaf(ml[n].y, exp2_approx(ml[n].x - top), Ls);
+    M = top;
+  }
+  const float inv = Ls > 0.f ? __fdiv_rn(1.f, Ls) : 0.f;
+#pragma unroll 1
+  for (int cc = 0; cc < D / 32; ++cc) {
+    float acc[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+#pragma unroll 1
+    for (int n0 = 0; n0 < np; n0 += 3) {
+      float4 v[3][8];
+      float f[3];
+#pragma unroll
+      for (int n = 0; n < 3; ++n)
+        if (n0 + n < np) {
+          f[n] = __ldcg(mls + (n0 + n) * kRows).x;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            v[n][q] = __ldcg(parts + ((n0 + n) * (D / 4) + 8 * cc + q) * kRows);
+        }
+#pragma unroll
+      for (int n = 0; n < 3; ++n)
+        if (n0 + n < np) {
+          const float w = exp2_approx(f[n] - M);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            acc[4 * q] = fmaf(v[n][q].x, w, acc[4 * q]);
+            acc[4 * q + 1] = fmaf(v[n][q].y, w, acc[4 * q + 1]);
+            acc[4 * q + 2] = fmaf(v[n][q].z, w, acc[4 * q + 2]);
+            acc[4 * q + 3] = fmaf(v[n][q].w, w, acc[4 * q + 3]);
+          }
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = pack_bf16x2(__fmul_rn(acc[8 * q + 2 * e], inv), __fmul_rn(acc[8 * q + 2 * e + 1], inv));
+      *reinterpret_cast<uint4*>(out + 32 * cc + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
 // The four softmax warps of a half meet; true when `v` is true of any of them.
 __device__ __forceinline__ bool half_any(int h, bool v) {
   int r;
@@ -1071,11 +1150,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   const uint32_t b_drain = smem_addr(&bars->drain);
   pdl_enter();  // the plan, q, k and v are written by kernels ahead in the stream
   const PlanHeader hdr = *reinterpret_cast<const PlanHeader*>(a.plan);
+  const int2 range = cta_pieces(a, blockIdx.x);  // (loaded with the header: one trip to L2 less)
   if (!plan_ok(hdr, a.want)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(err.word, kErrRange);
     return;
   }
-  const int2 range = cta_pieces(a, blockIdx.x);
   if (range.x >= range.y) return;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -1094,6 +1173,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     }
     mbar_init(b_drain, 2);
     bars->abort_flag = 0;
+    bars->joins[0] = bars->joins[1] = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k);
@@ -1266,6 +1346,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     int tiles = 0;           // of the ring, before this piece
     uint32_t sn = 0;         // bit `place`: turn of s_full
     int dn = 0, on = 0;      // products so far: of any tile, of a piece's last
+    // Joins wait for the block's end (only its first and last piece can be of a split tile): in the
+    // loop their loads in flight would cost registers.
     bool ok = true;
     for (int pi = range.x; pi < range.y; ++pi) {
       const Piece p = load_piece(a, pi);
@@ -1376,9 +1458,24 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       // a partial result: [slot][D / 4][row][4], a warp's stores of four channels next to each other
       const int64_t prow = static_cast<int64_t>(p.slot) * a.row_cap + h * kHalfRows + r;
       float4* part = reinterpret_cast<float4*>(a.acc) + static_cast<int64_t>(p.slot) * a.row_cap * (D / 4) + h * kHalfRows + r;
-      bool last = p.slot < 0;
-      Split* sp = nullptr;
-      if (p.slot >= 0) {
+      if (p.slot < 0) {
+        const float inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o[32];
+          load_o<D>(to, cc, nj > 0, o);
+          if (!real) continue;
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_bf16x2(__fmul_rn(__uint_as_float(o[8 * q4 + 2 * e]), inv),
+                                 __fmul_rn(__uint_as_float(o[8 * q4 + 2 * e + 1]), inv));
+            *reinterpret_cast<uint4*>(orow + 32 * cc + 8 * q4) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      } else {
 #pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t o[32];
@@ -1392,71 +1489,31 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           }
         }
         if (real) a.ml[prow] = make_float2(m * c, l);
-        sp = split_of(a, p);
         __threadfence();  // the partial result ahead of its arrival
         half_any(h, false);
-        if (quad == 0 && lane == 0) bars->last[h] = atomicAdd(&sp->arrived[h], 1) == sp->pieces - 1;
-        half_any(h, false);
-        last = bars->last[h];
-        if (last) __threadfence();
-      }
-      if (last) {
-        // the whole row, of this piece alone or of all pieces in their order
-        const int np = sp != nullptr ? sp->pieces : 1, slot0 = sp != nullptr ? sp->slot0 : p.slot;
-        const float2* mls = a.ml + static_cast<int64_t>(slot0) * a.row_cap + h * kHalfRows + r;
-        const float4* parts =
-            reinterpret_cast<const float4*>(a.acc) + static_cast<int64_t>(slot0) * a.row_cap * (D / 4) + h * kHalfRows + r;
-        float M = m * c, Ls = l;
-        if (sp != nullptr && real) {
-          for (int n = 0; n < np; ++n) M = fmaxf(M, __ldcg(mls + static_cast<int64_t>(n) * a.row_cap).x);
-          Ls = 0.f;
-          for (int n = 0; n < np; ++n) {
-            const float2 ml = __ldcg(mls + static_cast<int64_t>(n) * a.row_cap);
-            Ls = fmaf(ml.y, exp2_approx(ml.x - M), Ls);
+        if (quad == 0 && lane == 0) {
+          Split* sp = split_of(a, p);
+          const int slot0 = sp->slot0, pieces = sp->pieces, n = bars->joins[h];
+          if (atomicAdd(&sp->arrived[h], 1) == pieces - 1 && n < 2) {
+            bars->join[h][n] = {sp, slot0, pieces, p.tok0, p.ntok, p.kvh};
+            bars->joins[h] = n + 1;
           }
         }
-        const float inv = Ls > 0.f ? __fdiv_rn(1.f, Ls) : 0.f;
-#pragma unroll 1
-        for (int cc = 0; cc < D / 32; ++cc) {
-          uint32_t o[32];
-          load_o<D>(to, cc, nj > 0, o);
-          if (!real) continue;
-          if (sp != nullptr) {
-            float acc[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) acc[e] = 0.f;
-#pragma unroll 1
-            for (int n = 0; n < np; ++n) {
-              const float f = exp2_approx(__ldcg(mls + static_cast<int64_t>(n) * a.row_cap).x - M);
-              const bool own = slot0 + n == p.slot;
-              const float4* src = parts + (static_cast<int64_t>(n) * (D / 4) + 8 * cc) * a.row_cap;
-#pragma unroll
-              for (int q4 = 0; q4 < 8; ++q4) {
-                const float4 v = own ? make_float4(__uint_as_float(o[4 * q4]), __uint_as_float(o[4 * q4 + 1]),
-                                                   __uint_as_float(o[4 * q4 + 2]), __uint_as_float(o[4 * q4 + 3]))
-                                     : __ldcg(src + static_cast<int64_t>(q4) * a.row_cap);
-                acc[4 * q4] = fmaf(v.x, f, acc[4 * q4]);
-                acc[4 * q4 + 1] = fmaf(v.y, f, acc[4 * q4 + 1]);
-                acc[4 * q4 + 2] = fmaf(v.z, f, acc[4 * q4 + 2]);
-                acc[4 * q4 + 3] = fmaf(v.w, f, acc[4 * q4 + 3]);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(acc[e]);
-          }
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16x2(__fmul_rn(__uint_as_float(o[8 * q4 + 2 * e]), inv),
-                                 __fmul_rn(__uint_as_float(o[8 * q4 + 2 * e + 1]), inv));
-            *reinterpret_cast<uint4*>(orow + 32 * cc + 8 * q4) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        if (sp != nullptr && quad == 0 && lane == 0) sp->arrived[h] = 0;  // for the next layer on this plan
       }
       tc_fence_before();  // O has been read ahead of the weights that let the next piece overwrite it
+    }
+    // split tiles whose last piece was this block's
+    ok = !half_any(h, !ok);
+    for (int i = 0; ok && i < bars->joins[h]; ++i) {
+      const auto& t = bars->join[h][i];
+      const int tok = h * tqh + rt;
+      const int64_t row0 = static_cast<int64_t>(t.slot0) * a.row_cap;
+      __threadfence();
+      if (rt < tqh && tok < t.ntok)
+        join_row<D>(a.ml + row0 + h * kHalfRows + r,
+                    reinterpret_cast<const float4*>(a.acc) + row0 * (D / 4) + h * kHalfRows + r, t.pieces,
+                    a.out + static_cast<int64_t>(t.tok0 + tok) * a.ld_out + (t.kvh * G + rg) * D);
+      if (quad == 0 && lane == 0) t.split->arrived[h] = 0;  // for the next layer on this plan
     }
   }
   tc_fence_before();
