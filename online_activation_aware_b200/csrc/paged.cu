@@ -206,7 +206,8 @@ cudaError_t launch_qk_norm_rope_paged(const void* qkv, const PagedShape& s, cons
   while ((int64_t(1) << page_log2) < p.page_size) ++page_log2;
   // Four slots a group once that still gives every SM 32 warps; below, one slot a group (a decode
   // step is latency: the fewer in a row the better). 32 + 8 + 8 heads of 128, four slots and one:
-  // 64 tokens 10.0 and 8.2 us, 2048 tokens 18.5 and 20.2, 10000 tokens 51 and 61 (L2 flushed).
+  // 64 tokens 10.0 and 8.2 us, 2048 tokens 18.5 and 20.2, 10000 tokens 51 and 61 (L2 flushed); two, three and six
+  // slots are slower than four (the nine prompts above: 47, 43, 43 us against 41).
   const bool wide = s.tokens * slots * ln >= int64_t(num_sms) * 32 * 32 * 4;
   const int64_t per = wide ? 4 : 1;
   const int64_t threads = s.tokens * ((slots + per - 1) / per) * ln;
