@@ -20,7 +20,7 @@
 // 140 us without alternatives (5.6 TB/s), 167 with five (4.7 TB/s), 197 with twenty; 1500 x 131072
 // fp32 139 us with five (5.6 TB/s). Few rows are split over the blocks of a cluster (segments), whose
 // first block reads the others' sums and candidates from their shared memory: 8 x 50257 fp32 takes
-// 6.4 us without alternatives, 14.5 with twenty, whose sorts and insertions are a chain of shuffles.
+// 6.4 us without alternatives, 12.4 with twenty, whose sorts and insertions are a chain of shuffles.
 #include <type_traits>
 
 #include "attention_common.cuh"
@@ -420,13 +420,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   cluster_sync();  // no block leaves while its shared memory is read
 }
 
-// Segments a row is split in (a power of two, up to a cluster's blocks): enough blocks to fill the
-// GPU once, each with at least 4096 logits (less work than that is shorter than joining it).
-// Splitting further, to even out the last wave, costs more in candidates than it saves: 3000 x
-// 131072 bf16, top 5: 172 us whole, 197 in halves (measured with the threshold from merged lists).
-int logprob_segments(int64_t rows, int64_t vocab, int num_sms) {
+// Segments a row is split in (a power of two, up to a cluster's blocks): at most as many blocks as
+// fill three quarters of the GPU, each with at least one chunk. (131072 bf16, top 5: 300 rows take 35
+// us in two, 37 whole; 590 rows 52 in two, 45 whole. 8 x 50257 fp32, top 20: 12.4 us in sixteen, 14.5
+// in eight. More segments than fit at once, to even out a last wave, cost more in candidates than
+// they save: 1000 x 32000 bf16 37 us in two, 27 whole.)
+int logprob_segments(int64_t rows, int64_t row_bytes, int num_sms) {
   const int64_t slots = static_cast<int64_t>(num_sms) * (1024 / kThreads);
-  const int64_t want = std::min((slots + rows - 1) / rows, vocab / 4096);
+  const int64_t want = std::min(3 * slots / (4 * rows), row_bytes / (kChunk * 16));
   int n = 1;
   while (2 * n <= want && n < kMaxSegments) n *= 2;
   return n;
@@ -468,7 +469,7 @@ cudaError_t launch_token_logprobs(const void* logits, int dtype, int64_t rows, i
                                   const int64_t* tokens, int64_t top, float* logprob, float* entropy, int64_t* top_ids,
                                   float* top_lp, int num_sms, unsigned* err, cudaStream_t stream) {
   const Outs o{tokens, logprob, entropy, top_ids, top_lp, err};
-  const int segments = logprob_segments(rows, vocab, num_sms), v = static_cast<int>(vocab), k = static_cast<int>(top);
+  const int segments = logprob_segments(rows, vocab * (dtype == 2 ? 4 : 2), num_sms), v = static_cast<int>(vocab), k = static_cast<int>(top);
   if (dtype == 0) return launch_t(static_cast<const __nv_bfloat16*>(logits), rows, v, ld, k, o, segments, stream);
   if (dtype == 1) return launch_t(static_cast<const __half*>(logits), rows, v, ld, k, o, segments, stream);
   return launch_t(static_cast<const float*>(logits), rows, v, ld, k, o, segments, stream);
