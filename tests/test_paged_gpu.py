@@ -127,6 +127,21 @@ def test_few_tokens_per_sequence(new):
     check(Case([new] * 5, length, 8, 2, 128, 32, seed=new))       # no bound given: any sequence may be long
 
 
+@pytest.mark.parametrize("new,length,H,Hkv,D,opts", [
+    ([30], [9000], 4, 1, 64, {}), ([20, 5], [7001, 300], 8, 2, 128, {}), ([17], [30000], 2, 1, 128, {}),
+    ([200], [6000], 3, 1, 64, dict(window=3000, prefix=[500])), ([1, 90, 2], [5000, 4100, 2], 6, 1, 128, dict(softcap=20.0)),
+    ([1], [40000], 2, 1, 64, {}), ([2, 1], [2600, 9000], 16, 2, 128, dict(window=2000))])
+def test_few_tiles_over_a_long_context(new, length, H, Hkv, D, opts):
+    # tiles in many pieces, several of them joined by one block; a plan used again by the next layer
+    c = Case(new, length, H, Hkv, D, 64, seed=sum(length))
+    bound = max(new)
+    first = check(c, max_new=bound, **opts)
+    plan = c.plan(bound, opts.get("window", 0), opts.get("prefix"))
+    for _ in range(3):
+        again = ttq.paged_attention(c.qd, plan, c.kd, c.vd, c.td, softcap=opts.get("softcap", 0.0))
+        assert torch.equal(again[: sum(new)], first[: sum(new)])
+
+
 def test_rows_that_see_nothing():
     # empty caches, and more new tokens than positions: the first of them lie before the start
     c = Case([1, 3, 5, 40], [0, 0, 2, 17], 8, 2, 64, 16)
