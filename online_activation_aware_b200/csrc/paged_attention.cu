@@ -419,7 +419,13 @@ __device__ __forceinline__ Needed needed_keys(const Piece& p, int window) {
   return n;
 }
 
-__device__ __forceinline__ int key_tile(const Piece& p, int j) { return j < p.nA ? j : p.lo + (j - p.nA); }
+// The j-th key tile that a piece works on, j in [j0, j1): the newest first, since a distance bias is
+// largest there and the running maximum then seldom rises (the chunks with biases below: 49 us oldest
+// first, 45 this way, both before the cheaper map of scores).
+__device__ __forceinline__ int key_tile(const Piece& p, int j) {
+  const int i = p.j0 + p.j1 - 1 - j;
+  return i < p.nA ? i : p.lo + (i - p.nA);
+}
 
 // Pieces [first, end) of block `cta`.
 __device__ __forceinline__ int2 cta_pieces(const PagedArgs& a, int cta) {
@@ -861,7 +867,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
 // ---------------------------------------------------------------- many rows: tcgen05
 
 // Bound by the tensor cores: 4 D flop per row and visible key (4096 new tokens behind 12315, 40 heads on
-// 8: 1.2 PFLOP, 733 us at the measured burst rate; 1058 us here, 1.14 PFLOP/s, tensor pipe 53% and
+// 8: 1.2 PFLOP, 733 us at the measured burst rate; 1050 us here, 1.15 PFLOP/s, tensor pipe 53% and
 // special function units 40% active; back to back under the power cap 1260 us, where the cap's
 // rate would take 880). A block is 256 rows in two halves, so that a tile of keys in shared memory
 // serves both and one half's products run under the other's softmax (128 rows and two blocks an SM:
@@ -995,38 +1001,61 @@ __device__ __forceinline__ float weights(uint32_t (&sr)[kManyKeys], float c, flo
   return s.x + s.y;
 }
 
+// The same for |x| <= 1/4 (4e-7), where the scores of a cap of 30 or 50 mostly are.
+__device__ __forceinline__ constexpr float tanh_small(int i) {
+  return i == 0 ? 0.9999995828f : i == 1 ? -0.3332190812f : 0.1284161359f;
+}
+
+// A pair of raw products to scores inside the cap: s Q((s unit)^2), the scale to log2 units in Q.
+template <bool SMALL>
+__device__ __forceinline__ uint64_t cap_pair(uint64_t s, uint64_t unit2, float scale) {
+  constexpr int kDegree = SMALL ? 2 : 5;
+  const uint64_t x = mul2(s, unit2), z = mul2(x, x);
+  auto coef = [&](int i) { return scale * (SMALL ? tanh_small(i) : tanh_coef(i)); };
+  uint64_t q = pack2(coef(kDegree), coef(kDegree));
+#pragma unroll
+  for (int i = kDegree - 1; i >= 0; --i) q = fma2(q, z, pack2(coef(i), coef(i)));
+  return mul2(s, q);
+}
+
 // Raw products to scores in log2 units, capped and biased, of a row whose first key is at distance
-// d0: two at a time inside the cap; a warp that meets a score beyond it takes them one by one.
-__device__ __forceinline__ void map_scores(uint32_t (&sr)[kManyKeys], const ScoreMap& map, float slope, float d0,
-                                           bool real) {
-  float big = 0.f;
-  if (map.cap2 > 0.f) {
-#pragma unroll
-    for (int k = 0; k < kManyKeys; k += 2)
-      big = fmaxf(fmaxf(big, fabsf(__uint_as_float(sr[k]))), fabsf(__uint_as_float(sr[k + 1])));
-  }
-  const uint64_t slope2 = pack2(slope, slope), scale2 = pack2(map.scale, map.scale), unit2 = pack2(map.unit, map.unit);
-  if (map.cap2 > 0.f && __any_sync(0xffffffffu, real && !(big * map.unit <= 1.f))) {
-#pragma unroll
-    for (int k = 0; k < kManyKeys; ++k)
-      sr[k] = __float_as_uint(fmaf(slope, d0 + static_cast<float>(k), map(__uint_as_float(sr[k]))));
-    return;
-  }
-  const bool capped = map.cap2 > 0.f;
-#pragma unroll
-  for (int k = 0; k < kManyKeys; k += 2) {
-    const uint64_t s = pack2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1]));
-    uint64_t v = mul2(s, scale2);
-    if (capped) {
-      const uint64_t x = mul2(s, unit2), z = mul2(x, x);
-      uint64_t q = pack2(tanh_coef(5), tanh_coef(5));
-#pragma unroll
-      for (int i = 4; i >= 0; --i) q = fma2(q, z, pack2(tanh_coef(i), tanh_coef(i)));
-      v = mul2(v, q);
-    }
-    const float2 r = unpack2(fma2(pack2(d0 + static_cast<float>(k), d0 + static_cast<float>(k + 1)), slope2, v));
+// d0: two at a time inside the cap; a warp that meets a score beyond it takes them one by one. (24
+// ragged chunks of 1 - 300 tokens with a window: 34 us of attention as they are, 38 with biases, 44 with
+// a cap of 30, 46 with both; 55 with both and one polynomial for the whole cap.)
+__device__ __forceinline__ void map_scores(uint32_t (&sr)[kManyKeys], const ScoreMap& map, bool biased, float slope,
+                                           float d0, bool real) {
+  auto pair = [&](int k) { return pack2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])); };
+  auto put = [&](int k, uint64_t v) {
+    const float2 r = unpack2(v);
     sr[k] = __float_as_uint(r.x);
     sr[k + 1] = __float_as_uint(r.y);
+  };
+  if (map.cap2 > 0.f) {
+    float big4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kManyKeys; k += 2)
+      big4[(k >> 1) & 3] =
+          fmaxf(fmaxf(big4[(k >> 1) & 3], fabsf(__uint_as_float(sr[k]))), fabsf(__uint_as_float(sr[k + 1])));
+    const float x = fmaxf(fmaxf(big4[0], big4[1]), fmaxf(big4[2], big4[3])) * map.unit;
+    const uint64_t unit2 = pack2(map.unit, map.unit);
+    if (__any_sync(0xffffffffu, real && !(x <= 1.f))) {
+#pragma unroll
+      for (int k = 0; k < kManyKeys; ++k) sr[k] = __float_as_uint(map(__uint_as_float(sr[k])));
+    } else if (__any_sync(0xffffffffu, real && !(x <= 0.25f))) {
+#pragma unroll
+      for (int k = 0; k < kManyKeys; k += 2) put(k, cap_pair<false>(pair(k), unit2, map.scale));
+    } else {
+#pragma unroll
+      for (int k = 0; k < kManyKeys; k += 2) put(k, cap_pair<true>(pair(k), unit2, map.scale));
+    }
+  }
+  if (biased) {
+    // (the scale is in the capped scores already)
+    const float scale = map.cap2 > 0.f ? 1.f : map.scale;
+    const uint64_t scale2 = pack2(scale, scale), slope2 = pack2(slope, slope), base2 = pack2(slope * d0, slope * d0);
+#pragma unroll
+    for (int k = 0; k < kManyKeys; k += 2)
+      put(k, fma2(pair(k), scale2, fma2(pack2(static_cast<float>(k), static_cast<float>(k + 1)), slope2, base2)));
   }
 }
 
@@ -1130,7 +1159,8 @@ struct Turn {
   }
 };
 
-template <int D>
+// MAPPED: scores are capped or biased (without, the code of it would cost the plain form registers).
+template <int D, bool MAPPED>
 __global__ void __launch_bounds__(kManyThreads, 1)
     many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const PagedArgs a) {
@@ -1338,9 +1368,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t to = lanes + Lay::kColO + h * D;
     const ScoreMap map = score_map(a);
-    const bool mapped = a.cap > 0.f || a.slopes != nullptr;
     // scores enter the exponent as s * c (raw products), or as they are once mapped
-    const float c = mapped ? 1.f : a.scale_log2;
+    const float c = MAPPED ? 1.f : a.scale_log2;
     const float slack = kRescaleSlack / c;
     const int rt = r / G, rg = r % G;
     int tiles = 0;           // of the ring, before this piece
@@ -1361,7 +1390,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const bool real = rt < tqh && tok < p.ntok;
       const int head = p.kvh * G + rg;
       const int pos = p.p0 + tok;
-      const float slope = a.slopes != nullptr ? a.slopes[head] * kLog2e : 0.f;
+      const float slope = MAPPED && a.slopes != nullptr ? a.slopes[head] * kLog2e : 0.f;
       // every token of the half sees all of [sure_lo, sure_hi]
       const int sure_hi = p.p0 + h * tqh;
       const int sure_lo = hdr.window > 0 ? p.p0 + min(p.ntok, (h + 1) * tqh) - hdr.window : 0;
@@ -1381,7 +1410,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         for (int cc = 0; cc < kManyKeys / 32; ++cc)
           tmem_ld_32x32b_x32(ts + 32 * cc, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * cc]));
         tmem_ld_wait();
-        if (mapped) map_scores(sr, map, slope, static_cast<float>(k0 - pos), real);
+        if (MAPPED) map_scores(sr, map, a.slopes != nullptr, slope, static_cast<float>(k0 - pos), real);
         const bool sure = k0 >= sure_lo && k0 + kManyKeys - 1 <= sure_hi;
         if (!sure) {
           // visible: lo < k <= hi, or in the prefix (offsets into the tile)
@@ -1401,7 +1430,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (mx <= m + slack || !real) mx = m;  // (rows that are not there hold anything)
         if (__any_sync(0xffffffffu, mx != m ? 1 : 0)) {
           const float corr = exp2_approx((m - mx) * c);
-          if (j > 0) {
+          if (j > 0 && __any_sync(0xffffffffu, mx != m && m != -FLT_MAX ? 1 : 0)) {  // (else O is zero)
             // P_{j-1} V_{j-1} has landed (P_{j-2} V_{j-2} has: S_j came after it)
             if (!warp_all(mbar_wait(b_o + 8 * h, (dn - 1) & 1, err, abort_flag))) {
               ok = false;
@@ -1568,10 +1597,12 @@ cudaError_t launch_attention_d(PagedArgs a, const PagedShape& s, const PagePool&
   if (!encode_bf16_tmap_3d(&tq, a.q, D, s.heads, s.tokens, D * 2, static_cast<uint64_t>(a.ld_q) * 2, 64,
                            static_cast<uint32_t>(a.G), static_cast<uint32_t>(kHalfRows / a.G)))
     return cudaErrorInvalidValue;
-  e = prepare_kernel(many_rows_kernel<D>, ManyLayout<D>::kSmem);
-  if (e == cudaSuccess)
-    e = launch_pdl(many_rows_kernel<D>, grid, dim3(kManyThreads), ManyLayout<D>::kSmem, stream, tq, tk, tv, a);
-  return e;
+  auto go = [&](auto kernel) {
+    cudaError_t e = prepare_kernel(kernel, ManyLayout<D>::kSmem);
+    if (e == cudaSuccess) e = launch_pdl(kernel, grid, dim3(kManyThreads), ManyLayout<D>::kSmem, stream, tq, tk, tv, a);
+    return e;
+  };
+  return a.cap > 0.f || a.slopes != nullptr ? go(many_rows_kernel<D, true>) : go(many_rows_kernel<D, false>);
 }
 
 }  // namespace

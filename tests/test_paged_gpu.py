@@ -230,6 +230,14 @@ def test_extreme_caps(softcap, max_new):
     check(Case([1, 1] if max_new else [1, 40], [200, 90], 8, 2, 128, 16, seed=4), max_new=max_new, softcap=softcap)
 
 
+@pytest.mark.parametrize("softcap", [4.0, 7.0, 12.0, 24.0, 100.0])
+@pytest.mark.parametrize("slopes", [None, [2.0 ** -i for i in range(8)]])
+def test_caps_around_the_scores(softcap, slopes):
+    # scores up to about 5: beyond the cap, inside it and far inside it, within one tile too
+    c = Case([130, 3, 64], [700, 200, 64], 8, 2, 128, 32, seed=int(softcap))
+    check(c, softcap=softcap, slopes=slopes)
+
+
 def test_padding_rows_and_neighbours_do_not_leak():
     # NaN in the padding rows of q and in another sequence's own cache stays where it is
     c = Case([3, 20, 1], [40, 300, 17], 8, 2, 128, 16, seed=12, pad=5)
