@@ -867,8 +867,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
 // ---------------------------------------------------------------- many rows: tcgen05
 
 // Bound by the tensor cores: 4 D flop per row and visible key (4096 new tokens behind 12315, 40 heads on
-// 8: 1.2 PFLOP, 733 us at the measured burst rate; 1050 us here, 1.15 PFLOP/s, tensor pipe 53% and
-// special function units 40% active; back to back under the power cap 1260 us, where the cap's
+// 8: 1.2 PFLOP, 733 us at the measured burst rate; 1050 us here, 1.15 PFLOP/s, tensor pipe 55% and
+// special function units 41% active; back to back under the power cap 1260 us, where the cap's
 // rate would take 880). A block is 256 rows in two halves, so that a tile of keys in shared memory
 // serves both and one half's products run under the other's softmax (128 rows and two blocks an SM:
 // 1758 us; this with one place of scores a half: 1197).
