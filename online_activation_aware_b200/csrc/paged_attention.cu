@@ -973,7 +973,8 @@ __device__ __forceinline__ float2 exp2_fma2(uint64_t y) {
 // returns their sum (before the rounding, whose errors average out over the row).
 // SURE: every score is a real one, so a fourth of the weights can go to exp2_fma2: the special
 // function unit takes eight cycles for a warp's exponentials, and with two warps on each it would
-// need all the time that the tensor cores do.
+// need all the time that the tensor cores do. (An eighth, a fifth, a fourth, a third, a half of them:
+// 1079, 1078, 1066, 1076, 1108 us for 4096 new tokens over 16k, L2 flushed.)
 template <bool SURE>
 __device__ __forceinline__ float weights(uint32_t (&sr)[kManyKeys], float c, float ref, uint32_t ts) {
   const uint64_t c2 = pack2(c, c), ref2 = pack2(ref, ref);
