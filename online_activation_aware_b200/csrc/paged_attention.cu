@@ -17,8 +17,8 @@
 //   many_rows_kernel tiles of up to 256 rows on tcgen05.
 // The pieces of a split tile leave partial results, and the block that leaves the last one joins
 // them (in the order of the pieces, whichever block that is, so that results repeat bit for bit).
-// Scores, maxima, sums and accumulators are fp32; the weights are rounded to bf16 for the second
-// product.
+// Scores, maxima, sums and accumulators are fp32; the second product takes the weights as two bf16
+// (few rows) or rounded to one (many rows, where a second one would be half as much work again).
 // Every mbarrier wait is bounded: a CTA that gives up records TTQ_ERR_TIMEOUT, drains what it
 // started and returns.
 #include <algorithm>
@@ -738,13 +738,18 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
         }
         // no visible key yet: a reference of zero keeps the weights of hidden keys at zero
         const float ref0 = m[0] == -FLT_MAX ? 0.f : m[0], ref1 = m[1] == -FLT_MAX ? 0.f : m[1];
-        uint32_t pa[4];
+        // a weight is the sum of two bf16, its rounded value and what that leaves: 2^-16 of it is lost,
+        // where the rounded value alone loses 2^-8 that the dense decode's fp32 weights keep (64
+        // sequences of 300 - 9000 positions, plan included: 132 us, 130 with one bf16; 3 of 60 - 131
+        // thousand: 178 and 174)
+        uint32_t pa[4], pr[4];
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
-          pa[2 * nb] = pack_bf16x2(exp2_approx(s[nb][0] - ref0), exp2_approx(s[nb][1] - ref0));
-          pa[2 * nb + 1] = pack_bf16x2(exp2_approx(s[nb][2] - ref1), exp2_approx(s[nb][3] - ref1));
-          l[0] += bf16lo_to_f32(pa[2 * nb]) + bf16hi_to_f32(pa[2 * nb]);
-          l[1] += bf16lo_to_f32(pa[2 * nb + 1]) + bf16hi_to_f32(pa[2 * nb + 1]);
+        for (int i = 0; i < 4; ++i) {
+          const float ref = i & 1 ? ref1 : ref0;
+          const float w0 = exp2_approx(s[i >> 1][2 * (i & 1)] - ref), w1 = exp2_approx(s[i >> 1][2 * (i & 1) + 1] - ref);
+          pa[i] = pack_bf16x2(w0, w1);
+          pr[i] = pack_bf16x2(w0 - bf16lo_to_f32(pa[i]), w1 - bf16hi_to_f32(pa[i]));
+          l[i & 1] += w0 + w1;
         }
         {
           // lanes 0-15: keys 0-15 of chunk c; lanes 16-31: of chunk c + 1
@@ -757,6 +762,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
             ldsm_x4_trans(rb + (ch >> 3) * Lay::kBox + (((ch & 7) ^ (row & 7)) << 4), b);
             mma_16816(o[2 * cc], pa, b[0], b[1]);
             mma_16816(o[2 * cc + 1], pa, b[2], b[3]);
+            mma_16816(o[2 * cc], pr, b[0], b[1]);
+            mma_16816(o[2 * cc + 1], pr, b[2], b[3]);
           }
         }
         __syncwarp();
