@@ -976,8 +976,21 @@ __device__ __forceinline__ float2 exp2_fma2(uint64_t y) {
                      __int_as_float(__float_as_int(pp.y) + (__float_as_int(tt.y) << 23)));
 }
 
+// a += low, b += high bf16 of a pair, in fp32.
+__device__ __forceinline__ void add_bf16_pair(uint32_t w, float& a, float& b) {
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "add.rn.f32.bf16 %0, lo, %0;\n\t"
+      "add.rn.f32.bf16 %1, hi, %1;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "r"(w));
+}
+
 // A row's weights 2^(s c + ref), rounded to bf16 and stored over its scores in tensor memory;
-// returns their sum (before the rounding, whose errors average out over the row).
+// returns the sum of the rounded weights, which is what the product takes: a row's reference lags its
+// maximum by up to kRescaleSlack, so one weight that takes all is no power of two, and its rounding
+// (2^-8) would show in the result if the sum had not lost it too. (4096 new tokens over 16k, passes
+// back to back: 1254 us, 1246 with the sum ahead of the rounding; 1288 with the pairs unpacked first.)
 // SURE: every score is a real one, so a fourth of the weights can go to exp2_fma2: the special
 // function unit takes eight cycles for a warp's exponentials, and with two warps on each it would
 // need all the time that the tensor cores do. (An eighth, a fifth, a fourth, a third, a half of them:
@@ -985,7 +998,7 @@ __device__ __forceinline__ float2 exp2_fma2(uint64_t y) {
 template <bool SURE>
 __device__ __forceinline__ float weights(uint32_t (&sr)[kManyKeys], float c, float ref, uint32_t ts) {
   const uint64_t c2 = pack2(c, c), ref2 = pack2(ref, ref);
-  uint64_t sum[2] = {0, 0};
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int cc = 0; cc < kManyKeys / 64; ++cc) {
     uint32_t w[32];
@@ -1001,12 +1014,11 @@ __device__ __forceinline__ float weights(uint32_t (&sr)[kManyKeys], float c, flo
         y.y = exp2_approx(y.y);
       }
       w[e] = pack_bf16x2(y.x, y.y);
-      sum[e & 1] = add2(sum[e & 1], pack2(y.x, y.y));
+      add_bf16_pair(w[e], sum[2 * (e & 1)], sum[2 * (e & 1) + 1]);
     }
     tmem_st_32x32b_x32(ts + 32 * cc, w);
   }
-  const float2 s = unpack2(add2(sum[0], sum[1]));
-  return s.x + s.y;
+  return (sum[0] + sum[2]) + (sum[1] + sum[3]);
 }
 
 // The same for |x| <= 1/4 (4e-7), where the scores of a cap of 30 or 50 mostly are.

@@ -52,3 +52,17 @@ def test_few_rows_weigh_values_like_the_dense_decode(new, length, H, Hkv):
     tol = 2.0 ** -15 * mag + 2.0 ** -8 * np.abs(want) + 1e-30
     worst = (np.abs(got.reshape(want.shape) - want) / tol).max()
     assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("new,length,max_new", [([1, 1, 1], [5, 700, 3000], 1), ([1, 130, 300, 20], [9, 700, 2500, 4000], None)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("opts", [dict(), dict(softcap=30.0), dict(slopes=True)])
+def test_equal_values_come_out_as_they_are(new, length, max_new, D, opts):
+    # peaked scores: most of a row's weight is on one key, far above the maximum of the tiles before it
+    c = Case(new, length, 8, 2, D, 16, seed=D + len(new), pad=0, scale=2.5)
+    value = (1 + torch.arange(2 * D) % 7 / 8).bfloat16().view(2, D)
+    c.vd = torch.where(torch.isnan(c.v), c.v, value.expand_as(c.v)).cuda()
+    if opts.get("slopes"):
+        opts = dict(slopes=torch.tensor([2.0 ** -(h + 4) for h in range(8)], device="cuda"))
+    got = attend(c, max_new, **opts).view(-1, 2, 4, D)
+    assert int((got != value.cuda().view(1, 2, 1, D)).sum()) == 0
