@@ -361,7 +361,9 @@ TTQ_API ttq_status ttq_prompt_attention(const void* qkv_bf16, int64_t T, int64_t
  *   window    0, or the number of positions a token sees at most: its own and the window - 1
  *             before it
  *   plan      device buffer of ttq_attention_plan_size() bytes: the plan and the scratch of
- *             ttq_paged_attention, so one call at a time may use it
+ *             ttq_paged_attention, so one call at a time may use it. A call that ended with
+ *             TTQ_ERR_TIMEOUT leaves no plan: the next one does no work and is reported as
+ *             TTQ_ERR_INVALID_ARG until ttq_attention_plan has made the plan again
  * Calls of ttq_paged_attention with this plan must be given the same sizes. seqs <= 65536;
  * tokens <= 2^24; kv_len <= 2^30. heads / kv_heads <= 64 (any integer). head_dim 64 or 128. */
 TTQ_API ttq_status ttq_attention_plan_size(int64_t seqs, int64_t tokens, int64_t max_new, int64_t heads,
@@ -462,11 +464,12 @@ TTQ_API ttq_status ttq_device_status(cudaStream_t stream);
  * after the call. A limit of 0 restores the default. */
 TTQ_API ttq_status ttq_set_wait_limit_ns(uint64_t ns);
 
-/* Test hook for failure detection: while enabled, every later launch of the tensor-core
- * kernel first waits on a barrier that nothing ever arrives at, so that wait runs out
- * after the limit set by ttq_set_wait_limit_ns; the kernel then records TTQ_ERR_TIMEOUT,
- * drains its own copies, frees its tensor memory and returns without writing Y. Used to
- * test the bounded waits; never enable it in production. */
+/* Test hook for failure detection: while enabled, every later launch of the linear's
+ * tensor-core kernel, and of ttq_paged_attention's kernels, first waits on a barrier that
+ * nothing ever arrives at, so that wait runs out after the limit set by
+ * ttq_set_wait_limit_ns; the kernel then records TTQ_ERR_TIMEOUT, drains its own copies,
+ * frees its tensor memory and returns without writing its output. Used to test the bounded
+ * waits; never enable it in production. */
 TTQ_API ttq_status ttq_debug_inject_stall(int32_t enable);
 
 /* Stage tracing for measurement. With n >= 6 event handles (cudaEvent_t created by the

@@ -364,7 +364,8 @@ def device_status(stream=None) -> int:
 
 
 def debug_inject_stall(enable: bool):
-    """Test hook: makes the tensor-core kernel wait on a barrier nothing arrives at."""
+    """Test hook: makes the linear's tensor-core kernel and paged attention wait on a barrier nothing
+    arrives at."""
     _check("ttq_debug_inject_stall", load_library().ttq_debug_inject_stall(1 if enable else 0))
 
 
@@ -575,7 +576,7 @@ class AttentionPlan:
     (default: ``tokens``) of them in one sequence. ``update`` plans a step from its lengths on
     the device, on the stream it is called on (in a captured graph it plans anew at every
     replay). The plan's buffer is also the scratch of ``paged_attention``: one call at a time
-    uses it."""
+    uses it, and after one that timed out ``update`` has to plan anew."""
 
     def __init__(self, seqs: int, tokens: int, heads: int, kv_heads: int, head_dim: int, max_new: int | None = None,
                  device="cuda"):

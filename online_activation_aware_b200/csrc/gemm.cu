@@ -619,6 +619,7 @@ cudaError_t launch_q(const Maps& mp, const KernelArgs& ka, int grid, size_t smem
 }  // namespace
 
 void set_inject_stall(bool on) { g_inject_stall = on; }
+bool stall_injected() { return g_inject_stall; }
 
 // Codes and group scale/zero rows can be TMA-loaded when their row pitches are 16-byte
 // multiples (every hidden size divisible by 128, with d / g divisible by 8).

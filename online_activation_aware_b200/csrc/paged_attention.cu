@@ -19,11 +19,13 @@
 // them (in the order of the pieces, whichever block that is, so that results repeat bit for bit).
 // Scores, maxima, sums and accumulators are fp32; the second product takes the weights as two bf16
 // (few rows) or rounded to one (many rows, where a second one would be half as much work again).
-// Every mbarrier wait is bounded: a CTA that gives up records TTQ_ERR_TIMEOUT, drains what it
-// started and returns.
+// Every mbarrier wait is bounded: a CTA that gives up records TTQ_ERR_TIMEOUT, marks the plan as
+// none (its counts of finished pieces are then incomplete, and a later layer would join pieces that
+// are not there), drains what it started once all its warps have stopped, and returns.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <cstddef>
 
 #include "attention_common.cuh"
 #include "ttq_internal.h"
@@ -49,6 +51,7 @@ struct PlanHeader {
   int pieces;
   int splits;      // (tile, key/value head)s of more than one piece
 };
+static_assert(offsetof(PlanHeader, magic) == 0, "forget_plan");
 
 // One piece of the keys of a tile of rows and a key/value head. Key tile j of [j0, j1) is tile j of
 // the cache when j < nA, else tile lo + (j - nA): a prefix apart from the window leaves a gap.
@@ -343,6 +346,7 @@ struct PagedArgs {
   float* acc;       // partial accumulators, unnormalised: [slot][row][D] (few rows), [slot][D / 4][row][4]
   float2* ml;       // their (maximum in log2 units, sum)
   int row_cap, G, stages;
+  int inject_stall;  // test hook: the products wait for a barrier that nothing arrives at
   const int* table;
   int width, num_pages, page_size, page_log2;
   float scale_log2;  // log2(e) / sqrt(D)
@@ -359,6 +363,11 @@ struct PagedArgs {
 __device__ __forceinline__ bool plan_ok(const PlanHeader& h, const PlanHeader& w) {
   return h.magic == kPlanMagic && h.seqs == w.seqs && h.tokens == w.tokens && h.max_new == w.max_new &&
          h.heads == w.heads && h.kv_heads == w.kv_heads && h.head_dim == w.head_dim;
+}
+
+// After a wait that ran out: calls on this plan are refused until it is made again.
+__device__ __forceinline__ void forget_plan(const PagedArgs& a) {
+  *reinterpret_cast<volatile unsigned*>(const_cast<uint8_t*>(a.plan)) = 0u;  // PlanHeader::magic
 }
 
 __device__ __forceinline__ Split* split_of(const PagedArgs& a, const Piece& p) {
@@ -550,8 +559,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
                                                                   const PagedArgs a) {
   using Lay = FewLayout<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bar_full[kFewMaxStages], bar_empty[kFewMaxStages];
-  __shared__ int abort_sh, last_sh;
+  __shared__ uint64_t bar_full[kFewMaxStages], bar_empty[kFewMaxStages], bar_stall;
+  __shared__ int abort_sh, last_sh, issued_sh;
   __shared__ float m_sh[4][kFewRows], l_sh[4][kFewRows];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -564,7 +573,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
       mbar_init(b_full + 8 * i, 1);
       mbar_init(b_empty + 8 * i, 4);
     }
+    mbar_init(smem_addr(&bar_stall), 1);
     abort_sh = 0;
+    issued_sh = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
@@ -616,17 +627,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
         }
       }
     }
-    if (lane == 0 && *abort_flag) {
-      // every copy this CTA started lands before its shared memory is released: the last use of
-      // every stage
-      for (int k = 0; k < min(issued, S); ++k) {
-        if (--st < 0) {
-          st = S - 1;
-          ph ^= 1;
-        }
-        attn_drain(b_full + 8 * st, ph, a.err);
-      }
-    }
+    if (lane == 0) issued_sh = issued;
   } else {
     // ------------------------------------------------------------ products: 16 keys of every tile
     const int r0 = lane >> 2, c0 = (lane & 3) * 2;
@@ -636,6 +637,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
     float* ex = reinterpret_cast<float*>(smem_raw + (base - raw) + S * Lay::kStage);
     Piece next = load_piece(a, range.x);
     bool ok = true;
+    if (a.inject_stall) ok = warp_all(mbar_wait(smem_addr(&bar_stall), 0, a.err, abort_flag));
     for (int pi = range.x; pi < range.y; ++pi) {
       const Piece p = next;
       if (pi + 1 < range.y) next = load_piece(a, pi + 1);
@@ -664,7 +666,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
       float m[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};
       // every token of the tile sees all of [sure_lo, p0]
       const int sure_lo = hdr.window > 0 ? p.p0 + p.ntok - hdr.window : 0;
-      for (int j = p.j0; j < p.j1; ++j) {
+      for (int j = p.j0; ok && j < p.j1; ++j) {
         if (!warp_all(mbar_wait(b_full + 8 * st, ph, a.err, abort_flag))) {
           ok = false;
           break;
@@ -868,7 +870,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
       few_any(false);  // the exchange is rewritten by the next piece
     }
   }
-  __syncthreads();  // every copy has landed or been drained
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) {
+    // every copy this CTA started lands before its shared memory is released: the last use of every
+    // stage (after the warps have met: the copies may all have been under way when the wait ran out)
+    forget_plan(a);
+    for (int k = max(issued_sh - S, 0); k < issued_sh; ++k) attn_drain(b_full + 8 * (k % S), k / S & 1, a.err);
+  }
 }
 
 // ---------------------------------------------------------------- many rows: tcgen05
@@ -902,9 +910,10 @@ struct ManyBars {
   uint64_t p_full[2][2];       // its weights are, in the same place
   uint64_t o_done[2];          // a product of a half with V has landed
   uint64_t o_full[2];          // the last one of a piece has
-  uint64_t drain;
+  uint64_t drain, stall;
   uint32_t tmem_base;
   int abort_flag;
+  int issued, q_loads;         // copies started, when the warp that starts them is done
   int joins[2];                // tiles that a half joins at the block's end
   struct {
     Split* split;
@@ -1222,7 +1231,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       mbar_init(b_of + 8 * i, 1);
     }
     mbar_init(b_drain, 2);
+    mbar_init(smem_addr(&bars->stall), 1);
     bars->abort_flag = 0;
+    bars->issued = bars->q_loads = 0;
     bars->joins[0] = bars->joins[1] = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm_q);
@@ -1294,16 +1305,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         z_v = z;
       }
     }
-    if (lane == 0 && *abort_flag) {
-      // every copy this CTA started lands before its shared memory is released
-      if (q_loads > 0) attn_drain(b_q, (q_loads - 1) & 1, err);
-      for (int k = 0; k < min(issued, S); ++k) {
-        if (--t.at < 0) {
-          t.at = S - 1;
-          t.ph ^= 1;
-        }
-        attn_drain(b_full + 8 * t.at, t.ph, err);
-      }
+    if (lane == 0) {
+      bars->issued = issued;
+      bars->q_loads = q_loads;
     }
   } else if (warp >= 9) {
     // ------------------------------------------------------------ products of a half
@@ -1318,6 +1322,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     int qn = 0;             // uses so far of q_full
     uint32_t pn = 0;        // bit `place`: turn of p_full
     bool ok = true;
+    if (a.inject_stall) ok = warp_all(mbar_wait(smem_addr(&bars->stall), 0, err, abort_flag));
     for (int pi = range.x; ok && pi < range.y; ++pi) {
       const Piece p = load_piece(a, pi);
       const int nj = p.j1 - p.j0;
@@ -1567,6 +1572,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) {
+    // every copy this CTA started lands before its shared memory is released (see few_rows_kernel)
+    forget_plan(a);
+    if (bars->q_loads > 0) attn_drain(b_q, (bars->q_loads - 1) & 1, err);
+    for (int k = max(bars->issued - S, 0); k < bars->issued; ++k) attn_drain(b_full + 8 * (k % S), k / S & 1, err);
+  }
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -1648,6 +1659,7 @@ cudaError_t launch_paged_attention(const void* q, int64_t ld_q, const PagedShape
   a.acc = reinterpret_cast<float*>(static_cast<uint8_t*>(plan) + l.off_acc);
   a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(plan) + l.off_ml);
   a.row_cap = l.row_cap;
+  a.inject_stall = stall_injected() ? 1 : 0;
   a.G = static_cast<int>(s.heads / s.kv_heads);
   a.table = p.table;
   a.width = static_cast<int>(p.width);

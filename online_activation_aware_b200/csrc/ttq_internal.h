@@ -189,9 +189,11 @@ cudaError_t launch_gemm_reduce(const GemmArgs& a, const GemmPlan& plan, cudaStre
 cudaError_t launch_gemm(const GemmArgs& a, const GemmPlan& plan, const DevErr& err,
                         cudaStream_t stream);
 
-// Test hook: when on, the tensor-core kernel's MMA thread first waits on a barrier that
-// nothing arrives at, so its bounded wait runs out (see ttq_debug_inject_stall).
+// Test hook: when on, the MMA thread of the linear's tensor-core kernel and the warps of products
+// of paged attention first wait on a barrier that nothing arrives at, so that their bounded wait
+// runs out (see ttq_debug_inject_stall).
 void set_inject_stall(bool on);
+bool stall_injected();
 
 // 2-D row-major tensor map of `elem_bytes`-sized elements with a {box_cols, box_rows}
 // box and the given swizzle.
