@@ -25,7 +25,8 @@ class PagedCache:
     The bookkeeping (free pages, how many sequences hold each page) lives on the host; the page
     tables live on the device (``table`` [max_seqs, width] int32) and follow it. Pages that
     several sequences hold are never written: ``extend`` gives a sequence its own copy of a
-    shared last page first. Every call acts on the current stream."""
+    shared last page first. Every call acts on the current stream; one that raises leaves the
+    cache as it was."""
 
     def __init__(self, layers: int, pages: int, page_size: int, kv_heads: int, head_dim: int, max_seqs: int,
                  max_len: int, device="cuda"):
@@ -119,7 +120,8 @@ class PagedCache:
         if len(seqs) == 0 or len(set(seqs)) != len(seqs) or len(seqs) != len(counts):
             raise ValueError("one count for each of at least one distinct sequences")
         need = 0
-        left = {}   # sequences that hold a shared last page, less those that copy it here
+        left = {}   # holders of a shared last page, less those that copy it here
+        copying = set()
         for s, n in zip(seqs, counts):
             self._check(s)
             if n < 1:
@@ -133,43 +135,59 @@ class PagedCache:
                 if left.setdefault(last, self._held[last]) > 1:
                     left[last] -= 1
                     need += 1
+                    copying.add(s)
         if need > len(self._free):
             raise RuntimeError(f"{need} pages are needed, {len(self._free)} are free")
-        src, dst, where = [], [], []
-        for s, n in zip(seqs, counts):
-            mine = self._pages[s]
-            if self._length[s] % self.page_size and self._held[mine[-1]] > 1:
-                p = heapq.heappop(self._free)
-                self._held[p] = 1
-                self._held[mine[-1]] -= 1
-                src.append(mine[-1])
-                dst.append(p)
-                mine[-1] = p
-                where.append((s, len(mine) - 1, p))
-            self._length[s] += n
-            while len(mine) * self.page_size < self._length[s]:
-                p = heapq.heappop(self._free)
-                self._held[p] = 1
-                mine.append(p)
-                where.append((s, len(mine) - 1, p))
-        # one upload: copies, table entries, the step's starts, lengths and rows (each part padded to
-        # 16 bytes)
-        starts = [0]
-        for n in counts:
-            starts.append(starts[-1] + n)
-        parts = [src, dst, [s * self.width + i for s, i, _ in where], [p for _, _, p in where], starts,
-                 [self._length[s] for s in seqs], seqs]
-        flat, at = [], []
-        for part in parts:
-            at.append(len(flat))
-            flat += part + [0] * (-len(part) % 4)
-        up = self._upload(flat)
-        src_d, dst_d, idx_d, new_d, start_d, len_d, row_d = (up[a: a + len(part)] for a, part in zip(at, parts))
-        if src:
-            ttq.copy_pages(self.k, self.v, src_d, dst_d)
-        if where:
-            self.table.view(-1).index_copy_(0, idx_d.long(), new_d)
-        return start_d, len_d, self.table.index_select(0, row_d)
+        src, dst, where, taken, pages, lengths = [], [], [], [], {}, {}
+
+        def take():
+            taken.append(heapq.heappop(self._free))
+            return taken[-1]
+
+        # the bookkeeping follows once the device's part is under way: a call that raises leaves it as it was
+        try:
+            for s, n in zip(seqs, counts):
+                mine = pages[s] = list(self._pages[s])
+                if s in copying:
+                    src.append(mine[-1])
+                    mine[-1] = take()
+                    dst.append(mine[-1])
+                    where.append((s, len(mine) - 1, mine[-1]))
+                lengths[s] = self._length[s] + n
+                while len(mine) * self.page_size < lengths[s]:
+                    mine.append(take())
+                    where.append((s, len(mine) - 1, mine[-1]))
+            # one upload: copies, table entries, the step's starts, lengths and rows (each part padded to
+            # 16 bytes)
+            starts = [0]
+            for n in counts:
+                starts.append(starts[-1] + n)
+            parts = [src, dst, [s * self.width + i for s, i, _ in where], [p for _, _, p in where], starts,
+                     [lengths[s] for s in seqs], seqs]
+            flat, at = [], []
+            for part in parts:
+                at.append(len(flat))
+                flat += part + [0] * (-len(part) % 4)
+            up = self._upload(flat)
+            src_d, dst_d, idx_d, new_d, start_d, len_d, row_d = (up[a: a + len(part)] for a, part in zip(at, parts))
+            idx_d = idx_d.long()
+            rows = torch.empty(len(seqs), self.width, dtype=torch.int32, device=self.table.device)
+            if src:
+                ttq.copy_pages(self.k, self.v, src_d, dst_d)
+            if where:
+                self.table.view(-1).index_copy_(0, idx_d, new_d)
+            torch.index_select(self.table, 0, row_d, out=rows)
+        except BaseException:
+            for p in taken:
+                heapq.heappush(self._free, p)
+            raise
+        for p in src:
+            self._held[p] -= 1
+        for p in taken:
+            self._held[p] = 1
+        self._pages.update(pages)
+        self._length.update(lengths)
+        return start_d, len_d, rows
 
     def compact(self) -> int:
         """Moves the held pages to the lowest places, so that the pools end in one run of free
@@ -182,15 +200,16 @@ class PagedCache:
         mapping = list(range(self.pages))
         for p, h in zip(movers, holes):
             mapping[p] = h
-            self._held[h], self._held[p] = self._held[p], 0
-        for s in self._pages:
-            self._pages[s] = [mapping[p] for p in self._pages[s]]
-        self._free = list(range(len(held), self.pages))
         pad = -len(movers) % 4
         up = self._upload(movers + [0] * pad + holes + [0] * pad + mapping)
         n = len(movers) + pad
         ttq.copy_pages(self.k, self.v, up[: len(movers)], up[n: n + len(movers)])
         ttq.remap_pages(self.table, up[2 * n:], out=self.table)
+        for p, h in zip(movers, holes):  # (last, as in extend)
+            self._held[h], self._held[p] = self._held[p], 0
+        for s in self._pages:
+            self._pages[s] = [mapping[p] for p in self._pages[s]]
+        self._free = list(range(len(held), self.pages))
         return len(movers)
 
 
@@ -245,30 +264,54 @@ class PagedTTQDecoder(TTQDecoder):
         return self._plans[key]
 
     def _run_step(self, x, seqs, counts, prefill: bool, trace=None):
+        before = [(s, self.cache.length(s)) for s in seqs]
         start, length, pages = self.cache.extend(seqs, counts)
-        plan = self._plan(len(seqs), x.shape[0], max(counts)).update(start, length)
-        self._step = (start, length, pages, plan)
         try:
+            plan = self._plan(len(seqs), x.shape[0], max(counts)).update(start, length)
+            self._step = (start, length, pages, plan)
             return self._stack(x, prefill, trace)
+        except BaseException:
+            for s, n in before:  # positions that some layer may not have written
+                self.cache.truncate(s, n)
+            raise
         finally:
             self._step = None
 
+    def _check_rows(self, x):
+        if x.dim() != 2 or x.shape[1] != self.hidden or not x.is_contiguous():
+            raise ValueError(f"x must be contiguous [tokens, {self.hidden}], got {tuple(x.shape)}")
+        if x.dtype != torch.bfloat16:
+            raise TypeError(f"x must be bfloat16, got {x.dtype}")
+        if x.device != self.cache.k.device:
+            raise ValueError(f"x is on {x.device}, the cache on {self.cache.k.device}")
+
     def prefill(self, x, trace=None):
         """Embeddings [T, hidden] bf16 of a new prompt -> final-normed hidden [T, hidden]; its
-        sequence is ``prompt``. Ends every sequence of the prompt before it."""
+        sequence is ``prompt``. Ends every sequence of the prompt before it (unless x is refused); when
+        it fails underway there is no prompt."""
+        self._check_rows(x)
+        if x.shape[0] < 1:
+            raise ValueError("a prompt has at least one token")
         if x.shape[0] > self.max_len:
             raise ValueError(f"{x.shape[0]} tokens exceed the cache of {self.max_len}")
         if -(-x.shape[0] // self.cache.page_size) > self.cache.pages:
             raise RuntimeError(f"{x.shape[0]} tokens exceed {self.cache.pages} pages of {self.cache.page_size}")
         self.cache.clear()
         self.prompt = self.cache.new()
-        return self._run_step(x, [self.prompt], [x.shape[0]], True, trace)
+        try:
+            return self._run_step(x, [self.prompt], [x.shape[0]], True, trace)
+        except BaseException:
+            self.cache.clear()
+            self.prompt = None  # the layers' codes may be of two prompts
+            raise
 
     def step(self, seqs, x, counts=None, trace=None):
         """New tokens' embeddings x [sum counts, hidden], counts[i] (default one) of sequence
-        seqs[i] -> their final-normed hidden states."""
+        seqs[i] -> their final-normed hidden states. A step that raises leaves the sequences at
+        their length before it."""
         if self.prompt is None:
             raise RuntimeError("step needs a prefill first")
+        self._check_rows(x)
         seqs = list(seqs)
         counts = [1] * len(seqs) if counts is None else list(counts)
         if sum(counts) != x.shape[0]:

@@ -1,0 +1,95 @@
+"""The paged decoder after calls that fail: a step or a prompt that is refused, or that fails in one of
+its layers, leaves no positions that were never written, and no prompt that is half quantized."""
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import online_activation_aware_b200 as ttq
+from online_activation_aware_b200.paged import PagedTTQDecoder
+from test_paged_decoder_gpu import SHAPE, build, tokens
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    ttq.load_library()
+    yield
+    assert ttq.device_status() == 0
+
+
+def make(**kw):
+    return build(PagedTTQDecoder, **{**dict(max_len=128, pages=24, page_size=16, max_seqs=4), **kw})
+
+
+def state(dec):
+    c = dec.cache
+    return c.free_pages, c.sequences, [c.page_list(s) for s in c.sequences], [c.length(s) for s in c.sequences]
+
+
+def stop_at(layer):
+    def trace(li, name, t):
+        if li == layer and name == "attn":
+            raise torch.OutOfMemoryError("no memory")
+    return trace
+
+
+def wrong_rows(n):
+    """Rows that a step of n tokens has to refuse."""
+    good = tokens(n, 4)
+    return [(good.float(), TypeError), (good.cpu(), ValueError), (good[:, :-8].contiguous(), ValueError),
+            (torch.cat([good, good], 1)[:, ::2], ValueError), (good[0] if n == 1 else good.view(-1), ValueError)]
+
+
+def test_a_failed_step_leaves_the_sequences():
+    x, new = tokens(41, 3), tokens(3, 4)
+    want = make()
+    want.prefill(x)
+    wf = want.fork()[0]
+    w0, w1 = want.step([wf], new, [3]), want.step([want.prompt, wf], new[:2])
+    dec = make()
+    dec.prefill(x)
+    f = dec.fork()[0]
+    before = state(dec)
+    for bad, kind in wrong_rows(3):
+        with pytest.raises(kind):
+            dec.step([f], bad, [3])
+        assert state(dec) == before
+    for layer in (0, 1):
+        with pytest.raises(torch.OutOfMemoryError):
+            dec.step([f, dec.prompt], tokens(30, 5), [20, 10], trace=stop_at(layer))
+        after = state(dec)
+        # lengths as before; a branch may keep its own copy of the last page
+        assert after[1] == before[1] and after[3] == before[3]
+        assert [len(p) for p in after[2]] == [len(p) for p in before[2]]
+    with pytest.raises(torch.OutOfMemoryError):
+        dec._plan, plan = (lambda *a: stop_at(0)(0, "attn", None)), dec._plan
+        try:
+            dec.step([f], new, [3])
+        finally:
+            dec._plan = plan
+    assert state(dec)[3] == before[3]
+    assert torch.equal(dec.step([f], new, [3]), w0)
+    assert torch.equal(dec.step([dec.prompt, f], new[:2]), w1)
+
+
+def test_a_failed_prompt_leaves_none():
+    x, other, new = tokens(41, 3), tokens(20, 6), tokens(2, 4)
+    dec = make()
+    dec.prefill(x)
+    before = state(dec)
+    for bad, kind in wrong_rows(41) + [(x[:0], ValueError), (tokens(129, 3), ValueError)]:
+        with pytest.raises(kind):
+            dec.prefill(bad)
+        assert state(dec) == before and dec.prompt is not None     # refused: the prompt before is still there
+    want = make()
+    want.prefill(x)
+    assert torch.equal(dec.step([dec.prompt], new[:1]), want.step([want.prompt], new[:1]))
+    with pytest.raises(torch.OutOfMemoryError):
+        dec.prefill(other, trace=stop_at(1))
+    assert dec.prompt is None and dec.cache.sequences == [] and dec.cache.free_pages == dec.cache.pages
+    for call in (lambda: dec.step([0], new[:1]), lambda: dec.decode(new[:1]), dec.fork):
+        with pytest.raises(RuntimeError):
+            call()
+    assert torch.equal(dec.prefill(x), make().prefill(x))
