@@ -228,6 +228,7 @@ class PagedTTQDecoder(TTQDecoder):
         self._cache_args = (pages, page_size, max_seqs)
         super().__init__(shape, weights, final_norm, q, g, alpha, lam, r, max_len, eps, rope_base, device)
         self.lm_head = None if lm_head is None else ttq.TTQLinear(lm_head, q, g, alpha, lam)
+        self._head_ready = False  # the head's codes are of this prompt
 
     def _make_cache(self):
         pages, page_size, max_seqs = self._cache_args
@@ -297,6 +298,7 @@ class PagedTTQDecoder(TTQDecoder):
         if -(-x.shape[0] // self.cache.page_size) > self.cache.pages:
             raise RuntimeError(f"{x.shape[0]} tokens exceed {self.cache.pages} pages of {self.cache.page_size}")
         self.cache.clear()
+        self._head_ready = False
         self.prompt = self.cache.new()
         try:
             return self._run_step(x, [self.prompt], [x.shape[0]], True, trace)
@@ -339,9 +341,16 @@ class PagedTTQDecoder(TTQDecoder):
     def score(self, hidden, tokens, top: int = 0, prefill: bool = False):
         """Log probabilities of ``tokens`` (int64, one a row of the final-normed hidden states),
         entropies and the ``top`` alternatives, through the output head. ``prefill`` quantizes
-        the head from these rows (a prompt's); later calls reuse its codes."""
+        the head from these rows (a prompt's); later calls reuse its codes, until the next prompt."""
         if self.lm_head is None:
             raise RuntimeError("the decoder has no output head")
+        if not prefill and not self._head_ready:
+            raise RuntimeError("the output head has no codes of this prompt: score the prompt with prefill=True first")
         ws = self.workspace(hidden.shape[0])
-        logits = self.lm_head.prefill(hidden, ws=ws) if prefill else self.lm_head.decode(hidden, ws=ws)
+        if prefill:
+            self._head_ready = False
+            logits = self.lm_head.prefill(hidden, ws=ws)
+            self._head_ready = True
+        else:
+            logits = self.lm_head.decode(hidden, ws=ws)
         return ttq.token_logprobs(logits, tokens, top)

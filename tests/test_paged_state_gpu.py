@@ -1,11 +1,13 @@
 """The paged decoder after calls that fail: a step or a prompt that is refused, or that fails in one of
 its layers, leaves no positions that were never written, and no prompt that is half quantized."""
 
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import online_activation_aware_b200 as ttq
+from online_activation_aware_b200 import synthetic
 from online_activation_aware_b200.paged import PagedTTQDecoder
 from test_paged_decoder_gpu import SHAPE, build, tokens
 
@@ -93,3 +95,26 @@ def test_a_failed_prompt_leaves_none():
         with pytest.raises(RuntimeError):
             call()
     assert torch.equal(dec.prefill(x), make().prefill(x))
+
+
+def test_the_head_answers_with_codes_of_this_prompt_only():
+    head = synthetic.as_bf16(np.random.default_rng(9).normal(size=(1000, SHAPE["hidden"])) / 16).cuda()
+    tok = torch.arange(30, device="cuda")
+    dec = make(lm_head=head)
+    h = dec.prefill(tokens(30, 3))
+    with pytest.raises(RuntimeError):
+        dec.score(h, tok)                                   # no codes at all
+    first = dec.score(h, tok, top=3, prefill=True)
+    again = dec.score(h, tok, top=3)
+    assert (first["logprob"] - again["logprob"]).abs().max() <= 2 * 2.0 ** -5   # (bf16 logits of size up to 8)
+    other = dec.prefill(tokens(30, 6))
+    with pytest.raises(RuntimeError):
+        dec.score(other, tok)                               # codes of the prompt before
+    got = dec.score(other, tok, top=3, prefill=True)
+    want = make(lm_head=head)
+    want = want.score(want.prefill(tokens(30, 6)), tok, top=3, prefill=True)
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    with pytest.raises(TypeError):
+        dec.score(other.float(), tok, prefill=True)         # fails underway: the head has no codes
+    with pytest.raises(RuntimeError):
+        dec.score(other, tok)
