@@ -37,6 +37,7 @@ class PagedCache:
         self.k = torch.empty(layers, pages, page_size, kv_heads, head_dim, dtype=torch.bfloat16, device=device)
         self.v = torch.empty_like(self.k)
         self.table = torch.full((max_seqs, self.width), -1, dtype=torch.int32, device=device)
+        self._births = 0
         self.clear()
 
     def clear(self):
@@ -45,6 +46,7 @@ class PagedCache:
         self._held = [0] * self.pages              # sequences that hold each page
         self._pages = {}                           # sequence -> its pages
         self._length = {}
+        self._born = {}                            # which of all sequences that ever had the number
 
     @property
     def free_pages(self) -> int:
@@ -72,6 +74,8 @@ class PagedCache:
         for seq in range(self.max_seqs):
             if seq not in self._pages:
                 self._pages[seq], self._length[seq] = [], 0
+                self._births += 1
+                self._born[seq] = self._births
                 return seq
         raise RuntimeError(f"all {self.max_seqs} sequences are in use")
 
@@ -87,11 +91,11 @@ class PagedCache:
         return other
 
     def free(self, seq: int):
-        """Ends a sequence; pages that no other holds become free."""
+        """Ends a sequence; pages that no other holds become free, and so does its number."""
         self._check(seq)
         for p in self._pages.pop(seq):
             self._release(p)
-        del self._length[seq]
+        del self._length[seq], self._born[seq]
 
     def truncate(self, seq: int, length: int):
         """Drops the positions from ``length`` on (rejected tokens), with pages left without any."""
@@ -234,9 +238,24 @@ class PagedTTQDecoder(TTQDecoder):
         pages, page_size, max_seqs = self._cache_args
         self.cache = PagedCache(len(self.layers), pages, page_size, self.Hkv, self.D, max_seqs, self.max_len,
                                 self.device)
-        self.prompt = None
+        self._prompt = None   # (sequence, which of its number) once a prompt's codes are in the layers
         self._plans = {}
         self._needs, self._scratch = {}, None
+
+    @property
+    def prompt(self) -> int | None:
+        """The prompt's own sequence; None before a prefill and once that sequence was freed (its
+        branches go on, and its number may be another sequence's)."""
+        if self._prompt is None or self.cache._born.get(self._prompt[0]) != self._prompt[1]:
+            return None
+        return self._prompt[0]
+
+    def _own(self) -> int:
+        if self._prompt is None:
+            raise RuntimeError("a prefill comes first")
+        if self.prompt is None:
+            raise RuntimeError("the prompt's own sequence was freed")
+        return self.prompt
 
     def workspace(self, T: int):
         """One scratch buffer for steps of any number of rows: it grows to the largest need."""
@@ -299,19 +318,20 @@ class PagedTTQDecoder(TTQDecoder):
             raise RuntimeError(f"{x.shape[0]} tokens exceed {self.cache.pages} pages of {self.cache.page_size}")
         self.cache.clear()
         self._head_ready = False
-        self.prompt = self.cache.new()
+        seq = self.cache.new()
+        self._prompt = (seq, self.cache._born[seq])
         try:
-            return self._run_step(x, [self.prompt], [x.shape[0]], True, trace)
+            return self._run_step(x, [seq], [x.shape[0]], True, trace)
         except BaseException:
             self.cache.clear()
-            self.prompt = None  # the layers' codes may be of two prompts
+            self._prompt = None  # the layers' codes may be of two prompts
             raise
 
     def step(self, seqs, x, counts=None, trace=None):
         """New tokens' embeddings x [sum counts, hidden], counts[i] (default one) of sequence
         seqs[i] -> their final-normed hidden states. A step that raises leaves the sequences at
         their length before it."""
-        if self.prompt is None:
+        if self._prompt is None:
             raise RuntimeError("step needs a prefill first")
         self._check_rows(x)
         seqs = list(seqs)
@@ -322,18 +342,16 @@ class PagedTTQDecoder(TTQDecoder):
 
     def decode(self, x, trace=None):
         """The next token of the prompt's own sequence."""
-        if self.prompt is None:
-            raise RuntimeError("decode needs a prefill first")
-        return self.step([self.prompt], x, None, trace)
+        return self.step([self._own()], x, None, trace)
 
     def capture_decode(self):
         raise NotImplementedError("steps of a paged decoder take their pages from the host")
 
     def fork(self, seq: int | None = None, count: int = 1) -> list:
         """``count`` new sequences that continue ``seq`` (default: the prompt's)."""
-        if self.prompt is None:
-            raise RuntimeError("fork needs a prefill first")
-        return [self.cache.fork(self.prompt if seq is None else seq) for _ in range(count)]
+        if seq is None:
+            seq = self._own()
+        return [self.cache.fork(seq) for _ in range(count)]
 
     def free(self, seq: int):
         self.cache.free(seq)

@@ -118,3 +118,22 @@ def test_the_head_answers_with_codes_of_this_prompt_only():
         dec.score(other.float(), tok, prefill=True)         # fails underway: the head has no codes
     with pytest.raises(RuntimeError):
         dec.score(other, tok)
+
+
+@pytest.mark.parametrize("through_cache", [False, True])
+def test_a_freed_prompt_is_not_mistaken_for_another_sequence(through_cache):
+    new = tokens(2, 4)
+    dec = make()
+    dec.prefill(tokens(41, 3))
+    a = dec.fork()[0]
+    dec.step([a], new[:1])
+    (dec.cache if through_cache else dec).free(dec.prompt)
+    assert dec.prompt is None
+    b = dec.fork(a)[0]                                      # takes the prompt's number
+    assert b == 0 and dec.prompt is None
+    before = state(dec)
+    for call in (lambda: dec.decode(new[:1]), dec.fork):
+        with pytest.raises(RuntimeError):
+            call()
+    assert state(dec) == before
+    assert torch.equal(dec.step([a], new[1:]), dec.step([b], new[1:]))
