@@ -351,6 +351,10 @@ class PagedTTQDecoder(TTQDecoder):
         """``count`` new sequences that continue ``seq`` (default: the prompt's)."""
         if seq is None:
             seq = self._own()
+        self.cache.length(seq)  # (there is such a sequence)
+        left = self.cache.max_seqs - len(self.cache.sequences)
+        if count > left:
+            raise RuntimeError(f"{count} sequences are asked for, {left} of {self.cache.max_seqs} are free")
         return [self.cache.fork(seq) for _ in range(count)]
 
     def free(self, seq: int):

@@ -137,3 +137,15 @@ def test_a_freed_prompt_is_not_mistaken_for_another_sequence(through_cache):
             call()
     assert state(dec) == before
     assert torch.equal(dec.step([a], new[1:]), dec.step([b], new[1:]))
+
+
+def test_a_fork_of_more_than_there_is_room_for_makes_none():
+    dec = make()                                            # four sequences
+    dec.prefill(tokens(41, 3))
+    before = state(dec)
+    with pytest.raises(RuntimeError):
+        dec.fork(count=4)
+    with pytest.raises(KeyError):
+        dec.fork(3, count=4)
+    assert state(dec) == before
+    assert dec.fork(count=0) == [] and dec.fork(count=3) == [1, 2, 3]
