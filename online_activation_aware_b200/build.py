@@ -1,13 +1,14 @@
 """Builds libttq.so (the C-ABI library of the TTQ hot path) in-tree with nvcc for
-sm_100a, and ``_host.so`` (the Python module that passes torch tensors to its paged entry
-points) with the host compiler. Usage: ``python -m online_activation_aware_b200.build`` (or
-call ``build()``).
+sm_100a, and where torch is installed ``_host.so`` (the Python module that passes torch
+tensors to its paged entry points) with the host compiler. Usage:
+``python -m online_activation_aware_b200.build`` (or call ``build()``).
 
 Object files go to ``_build/`` at the repository root; the shared libraries are written
 next to this file so that the snapshot of the repository carries them."""
 
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -76,11 +77,16 @@ def build_host(verbose: bool = False, force: bool = False) -> str:
 
 
 def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
-    """Compiles every .cu under csrc/ and links libttq.so, and the host module beside it. Returns
-    the library path."""
-    build_host(verbose, force)
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
-        return LIB
+    """Compiles every .cu under csrc/ and links libttq.so, then the host module beside it (where torch
+    is installed: the C library needs nvcc only). Returns the library path."""
+    if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < _deps_mtime():
+        build_library(verbose, extra_flags)
+    if importlib.util.find_spec("torch") is not None:
+        build_host(verbose, force)
+    return LIB
+
+
+def build_library(verbose: bool = False, extra_flags=()) -> None:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
 
@@ -104,7 +110,6 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
