@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kWriteThreads) qk_norm_rope_paged_kernel(
   const int64_t t = item / static_cast<uint32_t>(groups);
   const int hs0 = static_cast<int>(item - static_cast<uint32_t>(t) * groups) * P;
   const int last = q_start[seqs];
-  if (q_start[0] != 0 || last > tokens) {
+  if (q_start[0] != 0 || last < 0 || last > tokens) {
     if (item == 0 && l == 0) atomicOr(err, kErrRange);
     if (q_start[0] != 0) return;
   }
@@ -79,8 +79,10 @@ __global__ void __launch_bounds__(kWriteThreads) qk_norm_rope_paged_kernel(
     }
   const unsigned mask = ((1u << LN) - 1u) << ((threadIdx.x & 31) / LN * LN);
   const int b = find_seq<LN>(q_start, seqs, static_cast<int>(t), l, mask);
-  const int64_t pos = static_cast<int64_t>(kv_len[b]) - q_start[b + 1] + t;
-  bool ok = pos >= 0 && pos < rope_rows;
+  const int begin = q_start[b], end = q_start[b + 1];
+  const int64_t pos = static_cast<int64_t>(kv_len[b]) - end + t;
+  // (starts that decrease leave a token without a sequence, or one that ends behind the last)
+  bool ok = begin <= t && t < end && end <= last && pos >= 0 && pos < rope_rows;
   int64_t row = 0;
   if (ok) {
     const int64_t pi = pos >> page_log2;
