@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <initializer_list>
 #include <optional>
@@ -40,7 +41,8 @@ struct Error {
   std::string text;
 };
 
-constexpr int64_t kAny = -1;  // any size
+constexpr int64_t kAny = -1;      // any size
+constexpr int64_t kMostTop = 32;  // alternatives of ttq_token_logprobs
 using Sizes = std::initializer_list<int64_t>;
 
 std::string sizes_text(const int64_t* s, size_t n) {
@@ -371,7 +373,7 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* tok = d.contiguous(tokens, "tokens", at::kLong, {rows});
     const On on(d, a[3]);
     at::Tensor lp = on.fresh({rows}, at::kFloat), ent = on.fresh({rows}, at::kFloat), ids, lps;
-    if (top > 0 && top <= vocab) {  // (the entry point refuses the others)
+    if (top > 0 && top <= std::min<int64_t>(vocab, kMostTop)) {  // (the entry point refuses the others)
       ids = on.fresh({rows, top}, at::kLong);
       lps = on.fresh({rows, top}, at::kFloat);
     }
