@@ -290,11 +290,10 @@ __global__ void __launch_bounds__(288) stats_tma_kernel(const __grid_constant__ 
         tma_load_2d(smem_addr(sm->tile[st]), &tm_x, full0 + 8 * st, x0,
                     static_cast<int>(r0 + static_cast<int64_t>(i) * kStatsTileRows));
       }
-      if (*abort_flag) {
-        // let every copy this block started land before its shared memory is released
-        for (int k = i > kStatsStages ? i - kStatsStages : 0; k < i; ++k)
-          mbar_drain_stats(full0 + 8 * (k % kStatsStages), (k / kStatsStages) & 1, err);
-      }
+      // every copy this block started lands before its shared memory is released (also when a
+      // consumer gives up after the last copy was started)
+      for (int k = i > kStatsStages ? i - kStatsStages : 0; k < i; ++k)
+        mbar_drain_stats(full0 + 8 * (k % kStatsStages), (k / kStatsStages) & 1, err);
     }
   } else {
     // ------------------------------------------------------------ consumers

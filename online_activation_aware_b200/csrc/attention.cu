@@ -173,13 +173,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnLayout<D, BK>::kMinBlocks)
 #pragma unroll
         for (int bx = 0; bx < D / 64; ++bx) tma_load_3d(vs + bx * kKVBox, &tm_v, b_vf + 8 * st, 64 * bx, hk, p0);
       }
-      if (*abort_flag) {
-        // every copy this CTA started lands before its shared memory is released
-        attn_drain(b_q, 0, err);
-        for (int k = j > 2 ? j - 2 : 0; k < j; ++k) {
-          attn_drain(b_kf + 8 * (k & 1), (k >> 1) & 1, err);
-          attn_drain(b_vf + 8 * (k & 1), (k >> 1) & 1, err);
-        }
+      // every copy this CTA started lands before its shared memory is released (also when another
+      // warp gives up after the last copy was started)
+      attn_drain(b_q, 0, err);
+      for (int k = j > 2 ? j - 2 : 0; k < j; ++k) {
+        attn_drain(b_kf + 8 * (k & 1), (k >> 1) & 1, err);
+        attn_drain(b_vf + 8 * (k & 1), (k >> 1) & 1, err);
       }
     }
   } else if (warp == 1) {

@@ -291,11 +291,10 @@ __global__ void __launch_bounds__(kThreads, MINB)
           }
         }
       }
-      if (*abort_flag) {
-        // let every copy this CTA started land before shared memory is released
-        for (uint32_t k = kc > S ? kc - S : 0; k < kc; ++k)
-          mbar_drain(bar_full + 8 * (k & (S - 1)), (k >> LOG2S) & 1, err);
-      }
+      // every copy this CTA started lands before shared memory is released (also when another warp
+      // gives up after the last copy was started)
+      for (uint32_t k = kc > S ? kc - S : 0; k < kc; ++k)
+        mbar_drain(bar_full + 8 * (k & (S - 1)), (k >> LOG2S) & 1, err);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer

@@ -134,11 +134,10 @@ __global__ void __launch_bounds__(lr_threads<NT, P>(), 2) lowrank_partial_kernel
         tma_load_2d(xs + kXBytes, &tm_a, bar_full + 8 * s, k0 + st * kLrK, 0);
         ++issued;
       }
-      if (*abort_flag) {
-        // every copy this block started lands before its shared memory is released
-        for (int st = issued > kLrStages ? issued - kLrStages : 0; st < issued; ++st)
-          lr_drain(bar_full + 8 * (st % kLrStages), (st / kLrStages) & 1, err);
-      }
+      // every copy this block started lands before its shared memory is released (also when a
+      // consumer gives up after the last copy was started)
+      for (int st = issued > kLrStages ? issued - kLrStages : 0; st < issued; ++st)
+        lr_drain(bar_full + 8 * (st % kLrStages), (st / kLrStages) & 1, err);
     }
     return;
   }
