@@ -412,14 +412,15 @@ TTQ_API ttq_status ttq_qk_norm_rope_paged(const void* qkv_bf16, int64_t seqs, in
  * compaction). Pools: `layers` layers of num_pages pages of page_bytes bytes each, contiguous.
  * Every destination appears once and is no source of another pair; a pair with src[i] == dst[i]
  * does nothing, a pair out of range is skipped and reported by ttq_device_status().
- *   src, dst  device int32 [pairs];  page_bytes % 16 == 0 */
+ *   src, dst  device int32 [pairs], 1 <= pairs <= num_pages;  page_bytes % 16 == 0 */
 TTQ_API ttq_status ttq_copy_pages(void* k_pool, void* v_pool, int64_t layers, int64_t num_pages, int64_t page_bytes,
                                   const int32_t* src, const int32_t* dst, int64_t pairs, cudaStream_t stream);
 
 /* out[i] = mapping[table[i]] for entries that are pages, table[i] for negative ones (the page
  * tables after a compaction). An entry past num_pages, or mapped past them, becomes -1 and is
  * reported by ttq_device_status().
- *   table, out  device int32 [entries] (out may be table);  mapping  device int32 [num_pages] */
+ *   table, out  device int32 [entries], entries >= 1 (out may be table);  mapping  device int32
+ *               [num_pages] */
 TTQ_API ttq_status ttq_remap_pages(const int32_t* table, int64_t entries, const int32_t* mapping, int64_t num_pages,
                                    int32_t* out, cudaStream_t stream);
 
@@ -436,7 +437,7 @@ typedef enum { TTQ_BF16 = 0, TTQ_FP16 = 1, TTQ_FP32 = 2 } ttq_dtype;
  *   top_ids  device int64 [rows, top], top_logprobs device fp32 [rows, top]; NULL when top = 0
  * A logit of -inf is a token of probability zero. A row with a NaN or +inf logit, or with
  * nothing but -inf, has NaN probabilities and entropy; its top_ids stay in the order of its
- * logits, NaN after everything else. 0 <= top <= min(32, vocab); vocab <= 2^20; rows < 2^31. */
+ * logits, NaN after everything else. 0 <= top <= min(32, vocab); vocab <= 2^20; 1 <= rows < 2^31. */
 TTQ_API ttq_status ttq_token_logprobs(const void* logits, ttq_dtype dtype, int64_t rows, int64_t vocab, int64_t ld,
                                       const int64_t* tokens, int64_t top, float* logprob, float* entropy,
                                       int64_t* top_ids, float* top_logprobs, cudaStream_t stream);

@@ -42,7 +42,7 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t 
   return d;
 }
 
-// 2^x (the hardware approximation; inputs are <= 0 here, -inf gives 0).
+// 2^x (the hardware approximation, off by 2^-22 of the value; -inf gives 0, results below 2^-126 are 0).
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -17,10 +17,11 @@
 //
 // Memory bound by its bytes (one read of the logits), but with 16-bit logits the exponentials alone
 // are 70% of that time (16 a cycle and SM), so sums and candidates show: 3000 x 131072 bf16 takes
-// 140 us without alternatives (5.6 TB/s), 167 with five (4.7 TB/s), 197 with twenty; 1500 x 131072
-// fp32 139 us with five (5.6 TB/s). Few rows are split over the blocks of a cluster (segments), whose
+// 138 us without alternatives (5.7 TB/s), 165 with five (4.8 TB/s), 196 with twenty, at full clock (171
+// to 183 with five in runs of seconds under the power cap); 1500 x 131072 fp32 138 us with five (5.7
+// TB/s). Few rows are split over the blocks of a cluster (segments), whose
 // first block reads the others' sums and candidates from their shared memory: 8 x 50257 fp32 takes
-// 6.4 us without alternatives, 12.4 with twenty, whose sorts and insertions are a chain of shuffles.
+// 4.2 us without alternatives, 10.0 with twenty (replayed from a graph), whose sorts and insertions are a chain of shuffles.
 #include <type_traits>
 
 #include "attention_common.cuh"
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 
 // Segments a row is split in (a power of two, up to a cluster's blocks): at most as many blocks as
 // fill three quarters of the GPU, each with at least one chunk. (131072 bf16, top 5: 300 rows take 35
-// us in two, 37 whole; 590 rows 52 in two, 45 whole. 8 x 50257 fp32, top 20: 12.4 us in sixteen, 14.5
+// us in two, 37 whole; 590 rows 52 in two, 45 whole. 8 x 50257 fp32, top 20: 10.0 us in sixteen, 12.5
 // in eight. More segments than fit at once, to even out a last wave, cost more in candidates than
 // they save: 1000 x 32000 bf16 37 us in two, 27 whole.)
 int logprob_segments(int64_t rows, int64_t row_bytes, int num_sms) {

@@ -47,7 +47,8 @@ constexpr int kWriteThreads = 128;
 // the arithmetic of a norm and a rotation is near it: two channels an instruction, few lanes a slot
 // (the norm's root and reciprocal are the same work however many lanes share them), and the
 // token's angles (64 bytes a lane) kept in registers for the group's slots. Nine prompts of 400 - 1900
-// tokens, 32 + 8 + 8 heads of 128 (169 MB): 36 us, 4.6 TB/s; 64 single tokens 2.9 us.
+// tokens, 32 + 8 + 8 heads of 128 (169 MB): 36 us a call, 4.7 TB/s; 64 single tokens 3.0 us, replayed
+// from a graph.
 template <int LN, int P>
 __global__ void __launch_bounds__(kWriteThreads) qk_norm_rope_paged_kernel(
     const __nv_bfloat16* __restrict__ qkv, int seqs, int tokens, int heads, int kv_heads,
@@ -207,9 +208,10 @@ cudaError_t launch_qk_norm_rope_paged(const void* qkv, const PagedShape& s, cons
   int page_log2 = 0;
   while ((int64_t(1) << page_log2) < p.page_size) ++page_log2;
   // Four slots a group once that still gives every SM 32 warps; below, one slot a group (a decode
-  // step is latency: the fewer in a row the better). 32 + 8 + 8 heads of 128, four slots and one:
-  // 64 tokens 10.0 and 8.2 us, 2048 tokens 18.5 and 20.2, 10000 tokens 51 and 61 (L2 flushed); two, three and six
-  // slots are slower than four (the nine prompts above: 47, 43, 43 us against 41).
+  // step is latency: the fewer in a row the better). 32 + 8 + 8 heads of 128, four slots and one, L2
+  // flushed ahead of each call: 64 tokens 10.0 and 8.2 us, 2048 tokens 18.5 and 20.2, 10000 tokens 51 and
+  // 61; two, three and six slots are slower than four (calls on the nine prompts above: 42, 38, 37 us
+  // against 36).
   const bool wide = s.tokens * slots * ln >= int64_t(num_sms) * 32 * 32 * 4;
   const int64_t per = wide ? 4 : 1;
   const int64_t threads = s.tokens * ((slots + per - 1) / per) * ln;

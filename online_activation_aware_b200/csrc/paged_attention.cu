@@ -500,8 +500,9 @@ constexpr int kFewThreads = 160;   // 4 warps of products, 1 of copies
 constexpr int kFewMaxStages = 8;
 
 // Bound by memory: K and V of every sequence are read once, for G rows of 4 D flop a key, which the
-// mma.sync units do on the side (64 sequences of 300 - 9000 positions, 32 heads on 8: 731 MB in 124 us,
-// 5.9 TB/s; 3 of 60 - 131 thousand, 64 on 8: 1.03 GB in 166 us, 6.2 TB/s). Every resident block has an
+// mma.sync units do on the side (64 sequences of 300 - 9000 positions, 32 heads on 8: 731 MB in 121 us,
+// 6.0 TB/s; 3 of 60 - 131 thousand, 64 on 8: 1.03 GB in 165 us, 6.2 TB/s; replayed from a graph, without
+// the plan). Every resident block has an
 // equal share of the step's key tiles, so a long sequence is spread over the GPU and short ones share
 // a block.
 //
@@ -882,9 +883,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
 // ---------------------------------------------------------------- many rows: tcgen05
 
 // Bound by the tensor cores: 4 D flop per row and visible key (4096 new tokens behind 12315, 40 heads on
-// 8: 1.2 PFLOP, 733 us at the measured burst rate; 1050 us here, 1.15 PFLOP/s, tensor pipe 55% and
-// special function units 41% active; back to back under the power cap 1260 us, where the cap's
-// rate would take 880). A block is 256 rows in two halves, so that a tile of keys in shared memory
+// 8: 1.2 PFLOP, 733 us at the measured burst rate; 1065 us here at full clock, 1.13 PFLOP/s, tensor
+// pipe 54% and special function units 41% active; 1150 - 1230 us in longer runs under the power cap,
+// whose rate would take 880). A block is 256 rows in two halves, so that a tile of keys in shared memory
 // serves both and one half's products run under the other's softmax (128 rows and two blocks an SM:
 // 1758 us; this with one place of scores a half: 1197).
 //
@@ -1003,7 +1004,7 @@ __device__ __forceinline__ void add_bf16_pair(uint32_t w, float& a, float& b) {
 // SURE: every score is a real one, so a fourth of the weights can go to exp2_fma2: the special
 // function unit takes eight cycles for a warp's exponentials, and with two warps on each it would
 // need all the time that the tensor cores do. (An eighth, a fifth, a fourth, a third, a half of them:
-// 1079, 1078, 1066, 1076, 1108 us for 4096 new tokens over 16k, L2 flushed.)
+// 1079, 1078, 1066, 1076, 1108 us for 4096 new tokens over 16k, one pass at a time, L2 flushed.)
 template <bool SURE>
 __device__ __forceinline__ float weights(uint32_t (&sr)[kManyKeys], float c, float ref, uint32_t ts) {
   const uint64_t c2 = pack2(c, c), ref2 = pack2(ref, ref);
@@ -1049,7 +1050,7 @@ __device__ __forceinline__ uint64_t cap_pair(uint64_t s, uint64_t unit2, float s
 
 // Raw products to scores in log2 units, capped and biased, of a row whose first key is at distance
 // d0: two at a time inside the cap; a warp that meets a score beyond it takes them one by one. (24
-// ragged chunks of 1 - 300 tokens with a window: 34 us of attention as they are, 38 with biases, 44 with
+// ragged chunks of 1 - 300 tokens with a window: 34 us of attention as they are, 39 with biases, 44 with
 // a cap of 30, 46 with both; 55 with both and one polynomial for the whole cap.)
 __device__ __forceinline__ void map_scores(uint32_t (&sr)[kManyKeys], const ScoreMap& map, bool biased, float slope,
                                            float d0, bool real) {
