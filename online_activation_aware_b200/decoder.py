@@ -96,7 +96,7 @@ class TTQDecoder:
         """Every layer over the rows of x; returns the final-normed hidden states."""
         T = x.shape[0]
         ws = self.workspace(T)
-        r = x.clone()
+        r = x.clone(memory_format=torch.contiguous_format)
         y = None
         for li, L in enumerate(self.layers):
             lin, nm = L["lin"], L["norms"]

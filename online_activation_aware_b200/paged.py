@@ -142,7 +142,7 @@ class PagedCache:
                     copying.add(s)
         if need > len(self._free):
             raise RuntimeError(f"{need} pages are needed, {len(self._free)} are free")
-        src, dst, where, taken, pages, lengths = [], [], [], [], {}, {}
+        src, dst, where, taken, own, added, lengths = [], [], [], [], {}, {}, {}
 
         def take():
             taken.append(heapq.heappop(self._free))
@@ -151,16 +151,17 @@ class PagedCache:
         # the bookkeeping follows once the device's part is under way: a call that raises leaves it as it was
         try:
             for s, n in zip(seqs, counts):
-                mine = pages[s] = list(self._pages[s])
+                held, new = len(self._pages[s]), []
                 if s in copying:
-                    src.append(mine[-1])
-                    mine[-1] = take()
-                    dst.append(mine[-1])
-                    where.append((s, len(mine) - 1, mine[-1]))
+                    own[s] = take()
+                    src.append(self._pages[s][-1])
+                    dst.append(own[s])
+                    where.append((s, held - 1, own[s]))
                 lengths[s] = self._length[s] + n
-                while len(mine) * self.page_size < lengths[s]:
-                    mine.append(take())
-                    where.append((s, len(mine) - 1, mine[-1]))
+                while (held + len(new)) * self.page_size < lengths[s]:
+                    new.append(take())
+                    where.append((s, held + len(new) - 1, new[-1]))
+                added[s] = new
             # one upload: copies, table entries, the step's starts, lengths and rows (each part padded to
             # 16 bytes)
             starts = [0]
@@ -189,7 +190,10 @@ class PagedCache:
             self._held[p] -= 1
         for p in taken:
             self._held[p] = 1
-        self._pages.update(pages)
+        for s, p in own.items():
+            self._pages[s][-1] = p
+        for s in seqs:
+            self._pages[s] += added[s]
         self._length.update(lengths)
         return start_d, len_d, rows
 
@@ -298,8 +302,8 @@ class PagedTTQDecoder(TTQDecoder):
             self._step = None
 
     def _check_rows(self, x):
-        if x.dim() != 2 or x.shape[1] != self.hidden or not x.is_contiguous():
-            raise ValueError(f"x must be contiguous [tokens, {self.hidden}], got {tuple(x.shape)}")
+        if x.dim() != 2 or x.shape[1] != self.hidden:
+            raise ValueError(f"x must be [tokens, {self.hidden}], got {tuple(x.shape)}")
         if x.dtype != torch.bfloat16:
             raise TypeError(f"x must be bfloat16, got {x.dtype}")
         if x.device != self.cache.k.device:
