@@ -596,6 +596,13 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(80)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc2(tmem, tmem_cols);
+    if (*abort_flag) {
+      // the same settling time for copies that were under way when another warp gave up later than
+      // the producer ended: this warp keeps the CTA's shared memory
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) {
+      }
+    }
   }
 }
 

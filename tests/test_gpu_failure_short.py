@@ -1,6 +1,7 @@
-"""A bounded wait of the linear's kernel of single CTAs that runs out while every copy of a CTA is already
-under way: few enough K blocks that the ring of stages is never full, so the warp that starts the
-copies has nothing to wait for. As in test_gpu_failure the kernel records TTQ_ERR_TIMEOUT, drains its copies and returns."""
+"""A bounded wait of the linear's kernels that runs out while every copy of a CTA is already under way:
+few enough K blocks that the ring of stages is never full, so the warp that starts the copies has
+nothing to wait for. As in test_gpu_failure the kernel records TTQ_ERR_TIMEOUT, lets its copies land
+and returns."""
 
 import pytest
 
@@ -14,7 +15,8 @@ pytestmark = pytest.mark.gpu
 TIMEOUT = -6
 
 
-@pytest.mark.parametrize("T,d,d_out", [(256, 256, 512), (300, 128, 264), (24, 512, 256), (40, 128, 72)])
+@pytest.mark.parametrize("T,d,d_out", [(256, 256, 512), (300, 128, 264), (24, 512, 256), (40, 128, 72),
+                                       (256, 512, 512), (300, 512, 264)])  # (the last two on CTA pairs)
 def test_a_wait_that_runs_out_behind_the_last_copy(T, d, d_out):
     X, W = synthetic.draw_layer(T, d, d_out, seed=5)
     Xb, Wb = synthetic.as_bf16(X).cuda(), synthetic.as_bf16(W).cuda()
